@@ -66,6 +66,24 @@ class vla_prefill_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in PREFILL_WEIGHT_FIELDS]
 
 
+class vla_kv8_config(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ["n_layers", "n_kv_heads", "head_dim", "capacity", "n_slots"]] +
+                [("flags", ctypes.c_uint)])
+
+
+class vla_kv8_rows(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ["slots", "pos", "count"]] +
+                [(n, ctypes.c_int) for n in ["layer", "n_layers", "batch", "n_tokens"]] +
+                [("stride", ctypes.c_longlong * 3)])
+
+
+class vla_kv8_query(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ["slots", "kv_len", "q_pos", "q_count"]] +
+                [(n, ctypes.c_int) for n in ["layer", "batch", "n_q", "n_heads", "causal", "window"]] +
+                [("scale", ctypes.c_float), ("q_stride", ctypes.c_longlong * 3),
+                 ("out_stride", ctypes.c_longlong * 3)])
+
+
 class vla_kernel_times(ctypes.Structure):
     _fields_ = [("total_ms", ctypes.c_float * 10), ("launches", ctypes.c_int * 10),
                 ("bytes", ctypes.c_double * 10), ("flops", ctypes.c_double * 10)]
@@ -106,6 +124,12 @@ _SIGNATURES = {
     "vla_pipeline_destroy": (None, [_P]),
     "vla_pipeline_submit": (_I, [_P, _P, _I, _P]),
     "vla_pipeline_step": (_I, [_P, _P, _P, _P, _P, _I, _P, _P]),
+    "vla_kv8_create": (_I, [ctypes.POINTER(vla_kv8_config), ctypes.POINTER(_P)]),
+    "vla_kv8_destroy": (None, [_P]),
+    "vla_kv8_write": (_I, [_P, _P, _P, ctypes.POINTER(vla_kv8_rows), _P]),
+    "vla_kv8_read": (_I, [_P, _P, _P, ctypes.POINTER(vla_kv8_rows), _P]),
+    "vla_kv8_attend": (_I, [_P, _P, _P, _P, ctypes.POINTER(vla_kv8_query), _P]),
+    "vla_kv8_status": (_I, [_P, _P]),
     "vla_last_error": (ctypes.c_char_p, []),
     "vla_version": (ctypes.c_char_p, []),
 }
@@ -208,6 +232,32 @@ def vla_pipeline_submit(h, tokens_ptr, n_tokens, stream):
 
 def vla_pipeline_step(h, K_ptr, V_ptr, noise_ptr, state_ptr, steps, out_ptr, stream):
     _check(load_library().vla_pipeline_step(h, K_ptr, V_ptr, noise_ptr, state_ptr, steps, out_ptr, stream))
+
+
+def vla_kv8_create(cfg: vla_kv8_config) -> int:
+    h = _P()
+    _check(load_library().vla_kv8_create(ctypes.byref(cfg), ctypes.byref(h)))
+    return h.value
+
+
+def vla_kv8_destroy(h: int):
+    load_library().vla_kv8_destroy(h)
+
+
+def vla_kv8_write(h, K_ptr, V_ptr, rows: vla_kv8_rows, stream):
+    _check(load_library().vla_kv8_write(h, K_ptr, V_ptr, ctypes.byref(rows), stream))
+
+
+def vla_kv8_read(h, K_ptr, V_ptr, rows: vla_kv8_rows, stream):
+    _check(load_library().vla_kv8_read(h, K_ptr, V_ptr, ctypes.byref(rows), stream))
+
+
+def vla_kv8_attend(h, q_ptr, out_ptr, lse_ptr, args: vla_kv8_query, stream):
+    _check(load_library().vla_kv8_attend(h, q_ptr, out_ptr, lse_ptr, ctypes.byref(args), stream))
+
+
+def vla_kv8_status(h, stream):
+    _check(load_library().vla_kv8_status(h, stream))
 
 
 def vla_device_status(h, stream):
@@ -426,6 +476,166 @@ class Pipeline:
             self.close()
         except Exception:
             pass
+
+
+class KVCache8:
+    """An 8-bit K/V cache: ``n_slots`` sequences of up to ``capacity`` tokens, ``n_layers`` layers
+    of ``n_kv_heads`` K/V heads of ``head_dim``, E4M3 values with a power-of-two scale for each
+    block of 64 tokens, on the current device. K, V, queries and outputs are CUDA tensors of
+    2-byte elements (bf16 values, as torch.bfloat16 or as bits in torch.int16); slots, pos,
+    count, kv_len, q_pos and q_count are CUDA int32 tensors [batch], read when the kernels run.
+    Calls run on the current stream; one stream at a time uses the cache. Rows that are out of
+    range on the device are left out and raise at the next ``status()``."""
+
+    def __init__(self, n_layers: int, n_kv_heads: int, head_dim: int, capacity: int, n_slots: int = 1):
+        import torch
+        c = vla_kv8_config()
+        c.n_layers, c.n_kv_heads, c.head_dim = int(n_layers), int(n_kv_heads), int(head_dim)
+        c.capacity, c.n_slots, c.flags = int(capacity), int(n_slots), 0
+        self.n_layers, self.n_kv_heads, self.head_dim = int(n_layers), int(n_kv_heads), int(head_dim)
+        self.capacity, self.n_slots = int(capacity), int(n_slots)
+        self.handle = vla_kv8_create(c)
+        self.device = torch.cuda.current_device()
+
+    def close(self):
+        if getattr(self, "handle", None):
+            vla_kv8_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # ---- argument checks: the library sees pointers only
+
+    def _index(self, t, batch, name):
+        if t is None:
+            return None
+        import torch
+        _expect(t, (batch,), name, torch.int32)
+        self._here(t, name)
+        return _dev_ptr(t, 4)
+
+    def _here(self, t, name):
+        if not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.device.index != self.device:
+            raise ValueError(f"{name}: on {t.device}, the cache is on cuda:{self.device}")
+
+    def _strided(self, t, shape, name):
+        """Pointer and the strides of all dims but the last, which must be dense (several
+        trailing dims in one, where ``shape`` joins them)."""
+        _expect(t, shape, name)
+        self._here(t, name)
+        import torch
+        if t.dtype not in (torch.bfloat16, torch.int16):
+            raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 (or its bits in int16)")
+        st = t.stride()
+        # the stride of a dim of one element (or of the last) says nothing: any value will do
+        if t.shape[-1] > 1 and st[-1] != 1:
+            raise ValueError(f"{name}: the last dim must be dense")
+        st = [s if n > 1 else 8 for s, n in zip(st[:-1], shape[:-1])]
+        if not any(st):
+            raise ValueError(f"{name}: every dim is expanded (all strides 0)")
+        return t.data_ptr(), st
+
+    def _rows(self, batch, n_tokens, layer, n_layers, pos, count, slots, strides):
+        r = vla_kv8_rows()
+        r.slots = self._index(slots, batch, "slots")
+        r.pos = self._index(pos, batch, "pos")
+        r.count = self._index(count, batch, "count")
+        r.layer, r.n_layers, r.batch, r.n_tokens = int(layer), int(n_layers), int(batch), int(n_tokens)
+        r.stride[:] = strides
+        return r
+
+    def write(self, K, V, pos=None, count=None, slots=None, layer: int = 0):
+        """K, V [n, batch, n_tokens, n_kv_heads * head_dim] (n layers from ``layer`` on; the last
+        dim dense, other strides multiples of 8). Row b's first count[b] tokens (all, without
+        count) go to the positions from pos[b] (0) of slot slots[b] (b). Tokens of the slot below
+        pos[b] stay, those behind the written ones are gone."""
+        if K.dim() != 4:
+            raise ValueError("K: expected [layers, batch, n_tokens, n_kv_heads * head_dim]")
+        n, batch, n_tok = (int(d) for d in K.shape[:3])
+        shape = (n, batch, n_tok, self.n_kv_heads * self.head_dim)
+        kp, ks = self._strided(K, shape, "K")
+        vp, vs = self._strided(V, shape, "V")
+        if ks != vs:
+            raise ValueError(f"K and V: strides {ks} and {vs}, expected the same")
+        vla_kv8_write(self.handle, kp, vp, self._rows(batch, n_tok, layer, n, pos, count, slots, ks), _stream())
+
+    def read(self, n_tokens: int, pos=None, count=None, slots=None, layer: int = 0, n_layers=None, batch=None,
+             K_out=None, V_out=None):
+        """Stored tokens as bf16: K, V [n_layers, batch, n_tokens, n_kv_heads * head_dim], int16
+        bits as Expert.set_prefix takes them unless K_out and V_out are given. Row b gets count[b]
+        tokens (n_tokens) from position pos[b] (0) of slot slots[b] (b); the output behind them is
+        left as it was (zeros in a tensor made here)."""
+        import torch
+        n = self.n_layers - int(layer) if n_layers is None else int(n_layers)
+        if batch is None:
+            given = [t for t in (K_out[0] if K_out is not None and K_out.dim() else None, slots, pos, count)
+                     if t is not None]
+            batch = int(given[0].shape[0]) if given else self.n_slots
+        shape = (n, int(batch), int(n_tokens), self.n_kv_heads * self.head_dim)
+        if (K_out is None) != (V_out is None):
+            raise ValueError("K_out and V_out go together")
+        if K_out is None:
+            if min(shape) < 1:
+                raise ValueError(f"K, V: no such shape {shape}")
+            dev = torch.device("cuda", self.device)
+            make = torch.empty if count is None else torch.zeros
+            K_out = make(shape, dtype=torch.int16, device=dev)
+            V_out = make(shape, dtype=torch.int16, device=dev)
+        kp, ks = self._strided(K_out, shape, "K_out")
+        vp, vs = self._strided(V_out, shape, "V_out")
+        if ks != vs:
+            raise ValueError(f"K_out and V_out: strides {ks} and {vs}, expected the same")
+        vla_kv8_read(self.handle, kp, vp, self._rows(batch, n_tokens, layer, n, pos, count, slots, ks), _stream())
+        return K_out, V_out
+
+    def attend(self, q, kv_len, layer: int = 0, slots=None, q_pos=None, q_count=None, causal: bool = False,
+               window: int = 0, scale=None, out=None, lse=None):
+        """softmax(scale * q K^T) V over one layer: q [batch, n_q, n_heads, head_dim] (the last dim
+        dense), n_heads a multiple of n_kv_heads; row b sees the first kv_len[b] tokens of slot
+        slots[b] (b). Query i stands at position q_pos[b] + i (without q_pos the queries are the
+        row's last tokens); ``causal`` hides the keys behind it, ``window`` w > 0 all but its last
+        w. Rows of ``out`` behind q_count[b] are left as they were (zeros in a tensor made here); a
+        query that sees no key gets zeros. ``lse``: optional fp32 [batch, n_q, n_heads] output,
+        log of the sum of exp(score). scale: 1 / sqrt(head_dim) unless given (> 0)."""
+        import torch
+        if q.dim() != 4:
+            raise ValueError("q: expected [batch, n_q, n_heads, head_dim]")
+        batch, n_q, n_heads = (int(d) for d in q.shape[:3])
+        if scale is not None and not float(scale) > 0.0:
+            raise ValueError("scale must be > 0")
+        shape = (batch, n_q, n_heads, self.head_dim)
+        qp, qs = self._strided(q, shape, "q")
+        if out is None:
+            out = (torch.empty if q_count is None else torch.zeros)(shape, dtype=q.dtype, device=q.device)
+        op, os_ = self._strided(out, shape, "out")
+        lp = None
+        if lse is not None:
+            _expect(lse, (batch, n_q, n_heads), "lse", torch.float32)
+            self._here(lse, "lse")
+            lp = _dev_ptr(lse, 4)
+        if kv_len is None:
+            raise ValueError("kv_len is required")
+        a = vla_kv8_query()
+        a.slots = self._index(slots, batch, "slots")
+        a.kv_len = self._index(kv_len, batch, "kv_len")
+        a.q_pos = self._index(q_pos, batch, "q_pos")
+        a.q_count = self._index(q_count, batch, "q_count")
+        a.layer, a.batch, a.n_q, a.n_heads = int(layer), batch, n_q, n_heads
+        a.causal, a.window = int(bool(causal)), int(window)
+        a.scale = 0.0 if scale is None else float(scale)
+        a.q_stride[:] = qs
+        a.out_stride[:] = os_
+        vla_kv8_attend(self.handle, qp, op, lp, a, _stream())
+        return out
+
+    def status(self):
+        vla_kv8_status(self.handle, _stream())
 
 
 class Expert:

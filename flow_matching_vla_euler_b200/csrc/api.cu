@@ -16,12 +16,14 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <new>
 #include <string>
 #include <tuple>
 #include <vector>
 
 #include "../../include/vla.h"
 #include "kernels.h"
+#include "kv8.cuh"
 
 using namespace vla;
 
@@ -1880,3 +1882,4 @@ int vla_gemm_status(void* cuda_stream) {
 
 #include "prefill_api.cuh"   // the prefix prefill handle, sharing this file's helpers
 #include "pipeline_api.cuh"  // the asynchronous prefill / denoise pipeline over both handles
+#include "kv8_api.cuh"       // the 8-bit K/V cache: write, read, attention

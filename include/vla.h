@@ -431,6 +431,104 @@ VLA_API int vla_pipeline_submit(vla_pipeline* p, const float* tokens, int n_toke
 VLA_API int vla_pipeline_step(vla_pipeline* p, const uint16_t* K_tok, const uint16_t* V_tok, const float* noise,
                               const float* state, int steps, float* out_actions, void* cuda_stream);
 
+/* ------------------------------------------------------------------- 8-bit K/V cache
+ *
+ * A store of K/V rows for many sequences (observations, prompts) in half the bytes of bf16,
+ * and softmax attention over it. Values are E4M3 with one fp32 scale for each block of 64
+ * tokens of a (layer, slot, K/V head), K and V apart: the smallest power of two
+ * s >= 2^-60 with max|x| / s <= 448; a value is stored as x / s rounded to the nearest E4M3
+ * value (ties to even) and stands for s * e4m3, which bf16 holds exactly up to its own
+ * range. A slot is one sequence of up to `capacity` tokens; the caller keeps the lengths.
+ * What vla_kv8_read returns has the layout that vla_cache_set_prefix takes and
+ * vla_prefill_run writes, so a prefilled prefix can wait in a slot until it is denoised
+ * against.
+ * Every call after create is stream-ordered, launches kernels only (no allocation, no host
+ * wait: it can be captured into a graph) and runs on the device the cache was created on,
+ * which must be the current one. The handle has one workspace: like every handle it is used
+ * by one stream at a time, and two captured graphs that use it must not run at once.
+ * slots, pos, count, kv_len, q_pos and q_count are DEVICE int32 arrays [batch], read when
+ * the kernels run. A row whose entries are out of range is left out (nothing of it is
+ * written) and reported by vla_kv8_status.
+ */
+typedef struct vla_kv8 vla_kv8;   /* opaque, owned by the library */
+
+typedef struct vla_kv8_config {
+  int n_layers;      /* L >= 1 */
+  int n_kv_heads;    /* K/V heads >= 1 */
+  int head_dim;      /* D: 32 (kept as 64), 64, 128 or 256 */
+  int capacity;      /* tokens a slot holds, >= 1 (kept in blocks of 64) */
+  int n_slots;       /* sequences, >= 1 */
+  unsigned flags;    /* 0 */
+} vla_kv8_config;
+
+/* Allocates the blocks (2 * L * n_slots * n_kv_heads * D bytes a token), their scales and the
+ * attention workspace on the current device; every token reads as 0. Synchronous. Errors:
+ * VLA_ERR_ARG, VLA_ERR_SHAPE, VLA_ERR_UNSUPPORTED (not sm_100), VLA_ERR_OOM, VLA_ERR_CUDA. */
+VLA_API int vla_kv8_create(const vla_kv8_config* cfg, vla_kv8** out);
+VLA_API void vla_kv8_destroy(vla_kv8* h);
+
+/* Rows of a write or a read. Row b holds count[b] tokens (count NULL: n_tokens) for the
+ * positions from pos[b] (pos NULL: 0) of slot slots[b] (slots NULL: b). The bf16 side is
+ * [n_layers][batch][n_tokens][n_kv_heads * D] with element strides stride[3] = (layer, row,
+ * token), multiples of 8, all 0 for a packed array; its layer 0 is the cache's `layer`. */
+typedef struct vla_kv8_rows {
+  const int *slots, *pos, *count;
+  int layer, n_layers;
+  int batch, n_tokens;
+  long long stride[3];
+} vla_kv8_rows;
+
+/*
+ * vla_kv8_write -- store DEVICE bf16 K and V rows. The tokens of a slot below pos[b] stay;
+ * what stood at pos[b] and behind it is gone (the slot now ends at pos[b] + count[b]). Where
+ * pos[b] lies inside a block, the block's scale is the larger of its old one and the one the
+ * new tokens need, and its kept tokens are rounded again to that scale (exact but for values
+ * that fall among E4M3's subnormals). A token of which a K or V value of one head is not
+ * finite is stored for that head as K = NaN, V = 0, and takes no part in the scales: a query
+ * that sees it gets NaN, one that does not is not touched by it. Two rows of one call must
+ * not name the same slot (the later one is left out and reported). K and V 16-byte aligned.
+ * Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE (layer, batch or n_tokens out of
+ * range), VLA_ERR_STATE (another device is current), VLA_ERR_CUDA.
+ */
+VLA_API int vla_kv8_write(vla_kv8* h, const uint16_t* K, const uint16_t* V, const vla_kv8_rows* rows,
+                          void* cuda_stream);
+
+/* vla_kv8_read -- the stored tokens as DEVICE bf16. Rows of the output behind count[b] are
+ * left as they were. Errors as vla_kv8_write. */
+VLA_API int vla_kv8_read(vla_kv8* h, uint16_t* K_out, uint16_t* V_out, const vla_kv8_rows* rows, void* cuda_stream);
+
+/* The queries of one attention call. */
+typedef struct vla_kv8_query {
+  const int *slots;          /* NULL: row b reads slot b; rows may share a slot */
+  const int *kv_len;         /* stored tokens of the row that may be seen, 0 .. capacity */
+  const int *q_pos;          /* position of the row's first query; NULL: kv_len - q_count (the
+                                queries are the row's last tokens, already written) */
+  const int *q_count;        /* queries of the row, 0 .. n_q; NULL: n_q */
+  int layer, batch, n_q, n_heads;   /* n_heads: a multiple of n_kv_heads; head h reads K/V head
+                                       h / (n_heads / n_kv_heads) */
+  int causal;                /* 1: query i sees keys j <= q_pos + i; 0: all below kv_len */
+  int window;                /* w > 0: only keys j > q_pos + i - w; 0: no window */
+  float scale;               /* of the scores; 0: 1 / sqrt(D) */
+  long long q_stride[3], out_stride[3];   /* elements (row, token, head), multiples of 8, all 0:
+                                             packed */
+} vla_kv8_query;
+
+/*
+ * vla_kv8_attend -- out = softmax(scale * q K^T) V over one layer of the cache. q, out: DEVICE
+ * bf16 [batch][n_q][n_heads][D], 16-byte aligned. A query that sees no key gets zeros. Output
+ * rows behind q_count[b] are left as they were. lse (optional, NULL: none): DEVICE fp32
+ * [batch][n_q][n_heads], the logarithm of the sum of exp(score) (-infinity: no key), with
+ * which the result can be joined with attention over other keys. Scores, maxima and sums are
+ * fp32. Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE, VLA_ERR_STATE (another device
+ * is current), VLA_ERR_CUDA; a bounded wait that gave up is reported by vla_kv8_status.
+ */
+VLA_API int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, const vla_kv8_query* args,
+                           void* cuda_stream);
+
+/* Synchronizes cuda_stream, then reads and clears the handle's device status word: VLA_OK,
+ * VLA_ERR_SHAPE (a row was out of range and left out), VLA_ERR_TIMEOUT or VLA_ERR_CUDA. */
+VLA_API int vla_kv8_status(vla_kv8* h, void* cuda_stream);
+
 /* Message of the last failed call on this thread ("" if none). Valid until the next call. */
 VLA_API const char* vla_last_error(void);
 

@@ -1,0 +1,414 @@
+"""The 8-bit K/V cache on the GPU (vla_kv8_* through the binding) against the fp64 model.
+
+Stored values are compared bit for bit (a rounding to nearest of an exact quotient). The
+attention's bound, element by element: the output's own rounding to bf16, half a step =
+2^-8 |o|; the weights' rounding, at most 2^-8 of each (the coarser of the two kernels: two
+E4M3 terms, each off by half a step 2^-4), and the scores' error e_s, both of which reach o
+through sum p |v| / sum p:
+    |err| <= 2^-8 |o| + (2^-8 + 2 e_s) * mean|v| (1 + 2^-7)
+                 + 448 * 2^-22 * top + 2^-133
+with e_s = scale * (D + 8) * 2^-23 * max_j sum_d |q_d k_jd| + 2^-20 (fp32 sums of exact
+products, truncated at worst; exp2 and the subtraction of the maximum, 2^-20 in all). The last
+terms are the ends of the number ranges: a weight times its V scale is held relative to the
+largest of the row, which is at least 1, with a smallest step of 2^-21 (E4M3's second term:
+2^-9 / 16 / 256; fp16's is 2^-24), so each of n keys adds at most 2^-22 of that largest times
+448 (top = n * largest weight * V scale); bf16 ends at 2^-133.
+"""
+import numpy as np
+import pytest
+import torch
+
+import flow_matching_vla_euler_b200 as V
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16(x):
+    """float64 numpy -> (bf16 CUDA tensor, its values in float64)."""
+    t = torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16)
+    return t.cuda(), t.double().numpy()
+
+
+def i32(x):
+    return None if x is None else torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def host(t):
+    t = t if t.dtype == torch.bfloat16 else t.view(torch.bfloat16)
+    return t.double().cpu().numpy()
+
+
+def kv_values(rng, shape):
+    x = rng.standard_normal(shape) * np.exp(0.7 * rng.standard_normal(shape[-1:]))
+    return x * np.exp(0.5 * rng.standard_normal(shape[:-1] + (1,)))
+
+
+class Pair:
+    """The cache and its model, written together."""
+
+    def __init__(self, L, kv, D, cap, S):
+        self.c = V.KVCache8(n_layers=L, n_kv_heads=kv, head_dim=D, capacity=cap, n_slots=S)
+        self.m = O.Kv8Model(L, kv, D, cap, S)
+
+    def write(self, K, V_, **kw):
+        kt, kn = bf16(K)
+        vt, vn = bf16(V_)
+        self.c.write(kt, vt, layer=kw.get("layer", 0), **{n: i32(kw.get(n)) for n in ("pos", "count", "slots")})
+        self.m.write(kn, vn, **kw)
+
+    def check_read(self, n_tokens, fill=-3.0, **kw):
+        n = kw.get("n_layers") or self.m.L - kw.get("layer", 0)
+        B = kw.get("batch") or len(next(kw[x] for x in ("slots", "pos", "count") if kw.get(x) is not None))
+        shape = (n, B, n_tokens, self.m.kv * self.m.D)
+        k = torch.full(shape, fill, dtype=torch.bfloat16, device="cuda")
+        v = torch.full(shape, fill, dtype=torch.bfloat16, device="cuda")
+        dev = {x: i32(kw.get(x)) for x in ("pos", "count", "slots")}
+        self.c.read(n_tokens, layer=kw.get("layer", 0), n_layers=n, batch=B, K_out=k, V_out=v, **dev)
+        self.c.status()
+        for w, t in ((0, k), (1, v)):
+            ref = self.m.read(w, n_tokens, fill=fill, **dict(kw, batch=B))
+            np.testing.assert_array_equal(host(t), ref)
+
+    def attend(self, Q, lens, lse=True, **kw):
+        qt, qn = bf16(Q)
+        out = torch.full(qt.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        ls = torch.full(qt.shape[:3], 9.0, dtype=torch.float32, device="cuda") if lse else None
+        dev = {x: i32(kw.get(x)) for x in ("slots", "q_pos", "q_count")}
+        rest = {x: kw[x] for x in ("layer", "causal", "window", "scale") if x in kw}
+        self.c.attend(qt, i32(lens), out=out, lse=ls, **dev, **rest)
+        self.c.status()
+        return qn, host(out), None if ls is None else ls.double().cpu().numpy()
+
+    def check_attend(self, Q, lens, **kw):
+        qn, got, ls = self.attend(Q, lens, **kw)
+        ref, rls, mean_v, mag, top = self.m.attend(qn, lens, fill=7.0, **kw)
+        scale = kw.get("scale") or 1.0 / np.sqrt(self.m.D)
+        es = (scale * (self.m.D + 8) * 2.0 ** -23 * mag + 2.0 ** -20)[..., None]
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * es) * mean_v * (1 + 2.0 ** -7)
+        tol += 448 * 2.0 ** -22 * top[..., None] + 2.0 ** -133
+        assert np.array_equal(np.isnan(got), np.isnan(ref))
+        err = np.where(np.isnan(ref), 0.0, np.abs(got - ref) - tol)
+        assert err.max() <= 0, f"err over bound {err.max():.3e}, max err {np.nanmax(np.abs(got - ref)):.3e}"
+        cnt = kw.get("q_count")
+        for b in range(ls.shape[0]):
+            n = ls.shape[1] if cnt is None else cnt[b]
+            assert np.all(ls[b, n:] == 9.0)
+            a, r = ls[b, :n], rls[b, :n]
+            assert np.array_equal(np.isneginf(a), np.isneginf(r)) and np.array_equal(np.isnan(a), np.isnan(r))
+            ok = np.isfinite(r)
+            assert np.all(np.abs(a[ok] - r[ok]) <= (es[b, :n, :, 0] + 2.0 ** -21 * np.abs(r) + 2.0 ** -20)[ok])
+
+
+SHAPES = [(1, 1, 256), (2, 3, 128), (1, 2, 64), (2, 2, 32)]
+
+
+# ---------------------------------------------------------------- write and read
+
+@pytest.mark.parametrize("L,kv,D", SHAPES)
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 200])
+def test_write_then_read(L, kv, D, n):
+    rng = np.random.default_rng(n * D)
+    p = Pair(L, kv, D, 211, 3)
+    p.write(kv_values(rng, (L, 2, n, kv * D)), kv_values(rng, (L, 2, n, kv * D)), slots=[2, 0])
+    p.check_read(n, slots=[2, 0])
+    p.check_read(211, batch=3)                       # slots never written read as zeros
+    if n > 5:
+        p.check_read(n - 4, slots=[0, 2], pos=[3, 4], count=[n - 4, 1])
+
+
+@pytest.mark.parametrize("L,kv,D", SHAPES)
+def test_ragged_writes_at_odd_positions(L, kv, D):
+    rng = np.random.default_rng(D)
+    p = Pair(L, kv, D, 300, 4)
+    p.write(kv_values(rng, (L, 4, 130, kv * D)), kv_values(rng, (L, 4, 130, kv * D)), count=[130, 1, 64, 77])
+    # pieces that start inside, at the end of and past blocks; growing and shrinking magnitudes
+    for step, f in enumerate((3.0, 0.01, 40.0)):
+        pos = [[130, 1, 64, 77], [131, 70, 100, 78], [63, 127, 128, 5]][step]
+        cnt = [[70, 69, 0, 1], [100, 1, 60, 100], [2, 65, 90, 100]][step]
+        p.write(f * kv_values(rng, (L, 4, 100, kv * D)), f * kv_values(rng, (L, 4, 100, kv * D)), pos=pos, count=cnt)
+        p.check_read(300, batch=4)
+
+
+def test_token_by_token_equals_the_model():
+    rng = np.random.default_rng(5)
+    p = Pair(2, 2, 64, 140, 2)
+    for t in range(140):
+        f = float(np.exp(rng.standard_normal()))
+        p.write(f * rng.standard_normal((2, 2, 1, 128)), f * rng.standard_normal((2, 2, 1, 128)), pos=[t, t],
+                slots=[1, 0])
+        if t % 23 == 0 or t == 139:
+            p.check_read(t + 1, batch=2)
+
+
+def test_extreme_values():
+    p = Pair(1, 1, 64, 64, 1)
+    x = np.zeros((1, 1, 8, 64))
+    x[0, 0, 0, 0], x[0, 0, 1, 0], x[0, 0, 2, 1], x[0, 0, 3, 2] = 448.0, 1.0, 2.0 ** -9, -2.0 ** -10
+    x[0, 0, 4], x[0, 0, 5, 5] = 1e-39, -447.0
+    p.write(x, -x)
+    p.check_read(8, batch=1)
+    big = np.full((1, 1, 3, 64), 2.5e38)
+    p.write(big, big, pos=[8])                       # the kept tokens fall to zero
+    p.check_read(11, batch=1)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_values_that_are_not_finite(bad):
+    rng = np.random.default_rng(3)
+    p = Pair(1, 2, 128, 200, 1)
+    K, Vv = kv_values(rng, (1, 1, 100, 256)), kv_values(rng, (1, 1, 100, 256))
+    K[0, 0, 10, 5] = bad                             # head 0
+    Vv[0, 0, 70, 200] = bad                          # head 1
+    Vv[0, 0, 99] = bad
+    p.write(K, Vv)
+    p.check_read(100, batch=1)
+    Q = rng.standard_normal((1, 100, 4, 128))
+    p.check_attend(Q, [100], causal=True)            # rows before a broken token are not touched
+    p.check_attend(Q[:, :3], [9])
+    p.check_attend(Q[:, :1], [100], causal=True, window=20)
+    p.write(rng.standard_normal((1, 1, 1, 256)), rng.standard_normal((1, 1, 1, 256)), pos=[64])
+    p.check_attend(Q[:, :2], [65], causal=True)      # what stands behind the length does not count
+    p.check_read(65, batch=1)
+
+
+def test_strided_rows():
+    rng = np.random.default_rng(8)
+    L, B, n, kv, D = 2, 3, 70, 2, 64
+    W = kv * D
+    p = Pair(L, kv, D, 80, B)
+    t, x = bf16(kv_values(rng, (n, L, B, 3 * W)))
+    K, Vv = t[..., W:2 * W].permute(1, 2, 0, 3), t[..., 2 * W:].permute(1, 2, 0, 3)
+    p.c.write(K, Vv)
+    p.m.write(x[..., W:2 * W].transpose(1, 2, 0, 3), x[..., 2 * W:].transpose(1, 2, 0, 3))
+    p.check_read(n, batch=B)
+    o = torch.full((n, L, B, 2 * W), 5.0, dtype=torch.bfloat16, device="cuda")
+    p.c.read(n, batch=B, K_out=o[..., :W].permute(1, 2, 0, 3), V_out=o[..., W:].permute(1, 2, 0, 3))
+    np.testing.assert_array_equal(host(o)[..., :W].transpose(1, 2, 0, 3), p.m.read(0, n, batch=B))
+    np.testing.assert_array_equal(host(o)[..., W:].transpose(1, 2, 0, 3), p.m.read(1, n, batch=B))
+    # one row for every slot (stride 0 of an input)
+    one, ov = bf16(kv_values(rng, (L, 1, n, W)))
+    p.c.write(one.expand(L, B, n, W), one.expand(L, B, n, W))
+    p.m.write(np.broadcast_to(ov, (L, B, n, W)), np.broadcast_to(ov, (L, B, n, W)))
+    p.check_read(n, batch=B)
+
+
+# ---------------------------------------------------------------- attention
+
+def _filled(rng, kv, D, cap, S, L=1):
+    p = Pair(L, kv, D, cap, S)
+    p.write(kv_values(rng, (L, S, cap, kv * D)), kv_values(rng, (L, S, cap, kv * D)))
+    return p
+
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 63, 64, 65, 257, 700])
+def test_one_token(D, n):
+    rng = np.random.default_rng(D + n)
+    p = _filled(rng, 2, D, n, 1)
+    p.check_attend(1.5 * rng.standard_normal((1, 1, 6, D)), [n])
+
+
+@pytest.mark.parametrize("group", [1, 3, 8, 16, 17, 24])
+def test_groups_of_heads(group):
+    rng = np.random.default_rng(group)
+    p = _filled(rng, 2, 64, 150, 3)
+    p.check_attend(rng.standard_normal((3, 1, 2 * group, 64)), [150, 1, 129], slots=[2, 2, 0], causal=True)
+
+
+@pytest.mark.parametrize("D,kv,H,nq", [(64, 4, 20, 5), (128, 2, 8, 50), (256, 1, 8, 50), (32, 1, 4, 17), (256, 2, 2, 7),
+                                       (128, 1, 3, 129), (64, 1, 1, 300)])
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 37), (False, 200)])
+def test_many_queries(D, kv, H, nq, causal, window):
+    rng = np.random.default_rng(nq + D + window)
+    p = _filled(rng, kv, D, 330, 2)
+    p.check_attend(rng.standard_normal((2, nq, H, D)), [330, 303], causal=causal, window=window)
+
+
+@pytest.mark.parametrize("nq", [4, 70])
+def test_ragged_counts_positions_and_empty_rows(nq):
+    rng = np.random.default_rng(nq)
+    p = _filled(rng, 2, 128, 200, 4, L=2)
+    Q = rng.standard_normal((6, nq, 8, 128))
+    # lengths of zero and one, no queries, queries before the first key and behind the last
+    lens, cnt = [0, 1, 200, 150, 64, 100], [nq, nq, 0, 3, 1, nq]
+    pos = [0, 0, 10, -2, 63, 150]
+    slots = [0, 1, 2, 3, 3, 0]
+    for causal, window in ((True, 0), (True, 5), (False, 0), (False, 30)):
+        p.check_attend(Q, lens, layer=1, slots=slots, q_pos=pos, q_count=cnt, causal=causal, window=window)
+
+
+def test_long_row_over_many_parts():
+    rng = np.random.default_rng(2)
+    p = _filled(rng, 1, 64, 20000, 2)
+    p.check_attend(rng.standard_normal((2, 1, 4, 64)), [20000, 77])
+    p.check_attend(rng.standard_normal((2, 1, 4, 64)), [64, 19999], scale=0.5)
+    p.check_attend(rng.standard_normal((2, 2, 20, 64)), [9999, 19999], causal=True, window=9000)
+
+
+def test_scores_of_unlike_size():
+    """Block scales far apart, scores far apart, one key that takes all."""
+    rng = np.random.default_rng(4)
+    p = Pair(1, 1, 128, 400, 1)
+    f = np.exp2(rng.integers(-40, 20, 7)).repeat(64)[:400, None]
+    p.write(rng.standard_normal((1, 1, 400, 128)), rng.standard_normal((1, 1, 400, 128)) * f)
+    Q = rng.standard_normal((1, 6, 2, 128)) * np.array([1e-30, 1e-3, 1.0, 5.0, 30.0, 1e3])[None, :, None, None]
+    p.check_attend(Q, [400])
+    p.check_attend(Q, [400], causal=True)
+    Q[0, :, 0, 3] *= 1e4
+    p.check_attend(Q, [390])
+    zero = Pair(1, 1, 128, 400, 1)                   # blocks of V that are all zero
+    zero.write(rng.standard_normal((1, 1, 400, 128)), np.where(f > 1, 0.0, f) * rng.standard_normal((1, 1, 400, 128)))
+    zero.check_attend(Q[:, :3], [400])
+
+
+def test_strided_queries_and_outputs():
+    rng = np.random.default_rng(6)
+    p = _filled(rng, 2, 64, 100, 3)
+    for nq in (1, 40):
+        t, x = bf16(rng.standard_normal((nq, 3, 3, 8, 64)))
+        q = t[:, :, 1].permute(1, 0, 2, 3)[:, :, ::2]
+        buf = torch.full((nq, 4, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = buf.permute(2, 0, 1, 3)
+        p.c.attend(q, i32([100, 99, 98]), causal=True, out=out)
+        ref, _, mean_v, _, _ = p.m.attend(x[:, :, 1].transpose(1, 0, 2, 3)[:, :, ::2], [100, 99, 98], causal=True)
+        assert np.all(np.abs(host(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7.9 * mean_v)
+
+
+def test_int16_bits_are_bf16():
+    rng = np.random.default_rng(7)
+    p = _filled(rng, 1, 64, 40, 1)
+    q, _ = bf16(rng.standard_normal((1, 3, 2, 64)))
+    a = p.c.attend(q, i32([40]))
+    b = p.c.attend(q.view(torch.int16), i32([40]))
+    assert b.dtype == torch.int16 and torch.equal(a.view(torch.int16), b)
+
+
+# ---------------------------------------------------------------- states, streams, graphs
+
+def test_rows_out_of_range_are_left_out_and_reported():
+    rng = np.random.default_rng(9)
+    p = _filled(rng, 1, 64, 100, 3)
+    K, _ = bf16(rng.standard_normal((1, 3, 10, 64)))
+    for kw in (dict(slots=[0, 3, 1]), dict(slots=[0, -1, 1]), dict(pos=[0, 91, 0]), dict(pos=[0, -1, 0]),
+               dict(count=[1, 11, 1]), dict(count=[1, -1, 1]), dict(slots=[2, 1, 2])):
+        p.c.write(K, K, **{k: i32(v) for k, v in kw.items()})
+        with pytest.raises(V.VlaError) as ei:
+            p.c.status()
+        assert ei.value.code == V.VLA_ERR_SHAPE
+        p.c.status()                                  # the word was cleared
+    # a refused row leaves its slot as it was
+    fresh = _filled(rng, 1, 64, 100, 3)
+    k, kn = bf16(rng.standard_normal((1, 3, 10, 64)))
+    fresh.c.write(k, k, slots=i32([2, 7, 2]))
+    fresh.m.write(kn[:, :1], kn[:, :1], slots=[2])
+    with pytest.raises(V.VlaError):
+        fresh.c.status()
+    fresh.check_read(100, batch=3)
+    for nq in (1, 60):
+        q, qn = bf16(rng.standard_normal((4, nq, 2, 64)))
+        out = torch.full_like(q, 7.0)
+        fresh.c.attend(q, i32([100, 101, -1, 50]), slots=i32([0, 1, 2, 3]), out=out)
+        with pytest.raises(V.VlaError):
+            fresh.c.status()
+        assert torch.all(out[1:] == 7.0)
+        ref, _, mean_v, _, _ = fresh.m.attend(qn[:1], [100])
+        assert np.all(np.abs(host(out[:1]) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7.9 * mean_v)
+
+
+def test_captured_calls_follow_the_device_arrays():
+    """A captured append and attend, replayed as the positions move on; bit-identical to the
+    same calls made one by one."""
+    rng = np.random.default_rng(10)
+    L, kv, D, H, B = 3, 2, 64, 8, 2
+    start = kv_values(rng, (L, B, 60, kv * D))
+    toks = kv_values(rng, (6, L, B, 1, kv * D))
+    qs = rng.standard_normal((6, L, B, 1, H, D))
+    eager, graph = Pair(L, kv, D, 100, B), Pair(L, kv, D, 100, B)
+    for p in (eager, graph):
+        p.write(start, start, count=[60, 33])
+    pos, length = i32([60, 33]), i32([61, 34])
+    K, _ = bf16(toks[0])
+    Q, _ = bf16(qs[0])
+    outs = torch.zeros((L, B, 1, H, D), dtype=torch.bfloat16, device="cuda")
+
+    def step(c, o):
+        for l in range(L):
+            c.write(K[l:l + 1], K[l:l + 1], pos=pos, layer=l)
+            c.attend(Q[l], length, layer=l, causal=True, out=o[l])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(graph.c, outs)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(graph.c, outs)
+    ref = torch.zeros_like(outs)
+    for i in range(6):
+        K.copy_(bf16(toks[i])[0])
+        Q.copy_(bf16(qs[i])[0])
+        pos.copy_(i32([60 + i, 33 + i]))
+        length.copy_(i32([61 + i, 34 + i]))
+        g.replay()
+        step(eager.c, ref)
+        torch.cuda.synchronize()
+        assert torch.equal(outs, ref), i
+    graph.c.status()
+    del g
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_a_call_gives_the_same_bits_again_and_on_another_stream(nq):
+    rng = np.random.default_rng(11)
+    p = _filled(rng, 2, 128, 3000, 3)
+    q, _ = bf16(rng.standard_normal((3, nq, 8, 128)))
+    lens = i32([3000, 17, 1500])
+    a = p.c.attend(q, lens, causal=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = p.c.attend(q, lens, causal=True)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_tensors_of_the_host_and_wrong_types_are_refused():
+    c = V.KVCache8(n_layers=1, n_kv_heads=1, head_dim=64, capacity=64, n_slots=2)
+    k = torch.zeros((1, 2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for call, err in [
+            (lambda: c.write(k.cpu(), k), TypeError), (lambda: c.write(k.float(), k), TypeError),
+            (lambda: c.write(k.half(), k), TypeError),
+            (lambda: c.write(k, k[:, :, :3]), ValueError), (lambda: c.write(k, k, pos=n.long()), TypeError),
+            (lambda: c.write(k, k, pos=n[:1]), ValueError), (lambda: c.write(k, k, pos=n.cpu()), TypeError),
+            (lambda: c.write(k[..., :32], k[..., :32]), ValueError),
+            (lambda: c.write(k[:, :, :, ::2], k), ValueError), (lambda: c.write(k, k, layer=1), V.VlaError),
+            (lambda: c.write(k.new_zeros((1, 3, 4, 64)), k.new_zeros((1, 3, 4, 64))), V.VlaError),
+            (lambda: c.write(k.new_zeros((1, 2, 65, 64)), k.new_zeros((1, 2, 65, 64))), V.VlaError),
+            (lambda: c.write(k[:1, :1, :1, :].expand(1, 2, 4, 64), k), ValueError),
+            (lambda: c.read(4, K_out=k), ValueError), (lambda: c.read(65), V.VlaError),
+            (lambda: c.read(0), ValueError), (lambda: c.read(4, layer=2), ValueError),
+            (lambda: c.read(4, layer=1, n_layers=1), V.VlaError),
+            (lambda: c.attend(q, None), ValueError), (lambda: c.attend(q, n.cpu()), TypeError),
+            (lambda: c.attend(q[..., :32], n), ValueError), (lambda: c.attend(q.float(), n), TypeError),
+            (lambda: c.attend(q, n, layer=1), V.VlaError), (lambda: c.attend(q, n, window=-1), V.VlaError),
+            (lambda: c.attend(q, n, scale=-1.0), ValueError), (lambda: c.attend(q, n, scale=float("inf")), V.VlaError),
+            (lambda: c.attend(q, n, out=q[:1]), ValueError),
+            (lambda: c.attend(q, n, lse=torch.zeros(2, 1, 4, device="cuda", dtype=torch.float64)), TypeError),
+            (lambda: c.attend(q, n, out=q[:, :, :1].expand(2, 1, 4, 64)), V.VlaError)]:
+        with pytest.raises(err):
+            call()
+    c.status()
+    two = V.KVCache8(n_layers=1, n_kv_heads=2, head_dim=64, capacity=64)
+    with pytest.raises(V.VlaError, match="multiple"):
+        two.attend(q[:1, :, :3], n[:1])
+    with pytest.raises(V.VlaError) as ei:
+        V.KVCache8(n_layers=1, n_kv_heads=1, head_dim=64, capacity=1 << 30, n_slots=16)
+    assert ei.value.code == V.VLA_ERR_SHAPE
+    c.close()
+    with pytest.raises(V.VlaError):
+        c.read(4)
