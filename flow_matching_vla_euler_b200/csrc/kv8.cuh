@@ -58,51 +58,165 @@ struct Kv8AttendParams {
   int layer, batch, n_q, n_heads, group;         // group = n_heads / n_kv
   int causal, window;
   float scale_log2;                    // softmax scale * log2(e)
-  int tiles;                           // row tiles per (row, K/V head)
-  float* ws;                           // partial outputs [2 * CTAs][tile rows][Ds]
-  float2* ws_ml;                       // [2 * CTAs][tile rows] (running maximum, sum)
+  int tile_rows, tiles;                // query rows of a tile, tiles of a (row, K/V head)
+  int unit;                            // blocks of 64 tokens in a unit of work
+  float* ws;                           // partial outputs [2 * CTAs][tile_rows][Ds]
+  float2* ws_ml;                       // [2 * CTAs][tile_rows] (reference maximum, sum)
   int grid;                            // CTAs of the attention kernel
   int* err;
 };
 
-// One batch row as the attention kernels see it.
-struct Kv8Row {
-  int slot, len, pos, cnt;             // slot < 0: refused or empty, nothing is written
-  int blk0, nblk;                      // blocks any of its queries can see (at least 1 if cnt > 0)
+// ---- the division of the work
+// An item is a tile of query rows of one (batch row, K/V head), its units the blocks that any
+// of its queries can see. All units stand in a line (batch row, tile, K/V head, block); CTA c
+// of `grid` takes the units [total * c / grid, total * (c + 1) / grid). So the CTAs have equal
+// work for any lengths, and at most two of a CTA's items are shared with others.
+
+struct Kv8Tile {
+  int slot, len, pos, cnt;             // slot < 0: refused, nothing of the row is written
+  int blk0, nblk, units;               // units 0: no queries in this tile
 };
 
-__device__ __forceinline__ Kv8Row kv8_row(const Kv8AttendParams& p, int b) {
-  Kv8Row r;
+__device__ __forceinline__ Kv8Tile kv8_tile(const Kv8AttendParams& p, int b, int tile) {
+  Kv8Tile r;
   r.slot = p.slots ? p.slots[b] : b;
   r.len = p.kv_len[b];
   r.cnt = p.q_count ? p.q_count[b] : p.n_q;
   r.pos = p.q_pos ? p.q_pos[b] : r.len - r.cnt;
-  r.blk0 = 0;
-  r.nblk = 0;
+  r.blk0 = r.nblk = r.units = 0;
   if (r.slot < 0 || r.slot >= p.c.n_slots || r.len < 0 || r.len > p.c.capacity || r.cnt < 0 || r.cnt > p.n_q ||
       r.pos < -p.n_q || r.pos > p.c.capacity) {
     r.slot = -1;
     r.cnt = 0;
     return r;
   }
-  if (r.cnt == 0) return r;
-  int hi = r.len, lo = 0;
-  if (p.causal) hi = min(hi, r.pos + r.cnt);
-  if (p.window) lo = max(0, r.pos - p.window + 1);
+  const int i0 = tile * p.tile_rows / p.group;
+  if (i0 >= r.cnt) return r;
+  const int i1 = min(r.cnt - 1, ((tile + 1) * p.tile_rows - 1) / p.group);
+  const int hi = p.causal ? min(r.len, r.pos + i1 + 1) : r.len;
+  const int lo = p.window ? max(0, r.pos + i0 - p.window + 1) : 0;
   r.blk0 = min(lo / kKv8Block, p.c.nblk - 1);
-  r.nblk = max(1, (hi + kKv8Block - 1) / kKv8Block - r.blk0);
+  r.nblk = max(1, (hi + kKv8Block - 1) / kKv8Block - r.blk0);   // one block even if no key is seen
+  r.units = (r.nblk + p.unit - 1) / p.unit;
   return r;
 }
 
 // Visible keys [lo, hi) of query token i of a row.
-__device__ __forceinline__ void kv8_seen(const Kv8AttendParams& p, const Kv8Row& r, int i, int& lo, int& hi) {
+__device__ __forceinline__ void kv8_seen(const Kv8AttendParams& p, const Kv8Tile& r, int i, int& lo, int& hi) {
   hi = p.causal ? min(r.len, r.pos + i + 1) : r.len;
   lo = p.window ? max(0, r.pos + i - p.window + 1) : 0;
 }
 
-// The few-rows kernel: 16 query rows a tile. tm_k, tm_v: the whole cache as rows of 64 bytes.
+// Sum over the CTA's threads, the same value in all of them (red: one slot per warp).
+__device__ __forceinline__ long long cta_sum(long long v, long long* red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  long long s = 0;
+  for (int i = 0; i < static_cast<int>(blockDim.x + 31) / 32; ++i) s += red[i];
+  return s;
+}
+
+__device__ __forceinline__ long long kv8_weight(const Kv8AttendParams& p, int e) {
+  if (e >= p.batch * p.tiles) return 0;
+  return static_cast<long long>(kv8_tile(p, e / p.tiles, e % p.tiles).units) * p.c.n_kv;
+}
+
+__device__ __forceinline__ long long kv8_total(const Kv8AttendParams& p, long long* red) {
+  long long n = 0;
+  for (int e = threadIdx.x; e < p.batch * p.tiles; e += blockDim.x) n += kv8_weight(p, e);
+  return cta_sum(n, red);
+}
+
+__device__ __forceinline__ long long part_begin(long long total, int grid, int c) { return total * c / grid; }
+
+// The (batch row, tile) entry that holds unit u < total, and the unit's number inside it.
+// Every warp of the CTA works it out for itself.
+__device__ __forceinline__ int kv8_find(const Kv8AttendParams& p, long long u, long long* inside) {
+  const int lane = threadIdx.x & 31;
+  long long at = 0;
+  for (int e = 0;; e += 32) {
+    const long long mine = kv8_weight(p, e + lane);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, at + inc > u);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      *inside = u - at - __shfl_sync(0xffffffffu, inc - mine, k);
+      return e + k;
+    }
+    at += __shfl_sync(0xffffffffu, inc, 31);
+    if (e + 32 >= p.batch * p.tiles) {   // u >= total: not reached
+      *inside = 0;
+      return 0;
+    }
+  }
+}
+
+// The segments of a CTA's part: its share of one item after the other.
+struct Kv8Segment {
+  Kv8Tile row;
+  int b, head, tile;
+  int blk, n;                     // blocks [blk, blk + n) of the slot
+  bool whole, first;              // the item's only part; the part that begins the CTA's range
+};
+
+struct Kv8Walk {
+  int e;
+  long long unit, left;
+  Kv8Tile row;
+  bool begun;
+};
+
+__device__ __forceinline__ Kv8Walk kv8_walk(const Kv8AttendParams& p, long long* red) {
+  Kv8Walk w;
+  const long long total = kv8_total(p, red);
+  const long long u0 = part_begin(total, p.grid, blockIdx.x);
+  w.left = part_begin(total, p.grid, blockIdx.x + 1) - u0;
+  w.begun = false;
+  w.e = 0;
+  w.unit = 0;
+  if (w.left) {
+    w.e = kv8_find(p, u0, &w.unit);
+    w.row = kv8_tile(p, w.e / p.tiles, w.e % p.tiles);
+  }
+  return w;
+}
+
+__device__ __forceinline__ bool kv8_next(const Kv8AttendParams& p, Kv8Walk& w, Kv8Segment& g) {
+  if (w.left == 0) return false;
+  while (w.unit >= static_cast<long long>(w.row.units) * p.c.n_kv) {
+    ++w.e;
+    w.unit = 0;
+    w.row = kv8_tile(p, w.e / p.tiles, w.e % p.tiles);
+  }
+  const int off = static_cast<int>(w.unit % w.row.units);
+  const int n = static_cast<int>(min(static_cast<long long>(w.row.units - off), w.left));
+  g.row = w.row;
+  g.b = w.e / p.tiles;
+  g.tile = w.e % p.tiles;
+  g.head = static_cast<int>(w.unit / w.row.units);
+  g.blk = w.row.blk0 + off * p.unit;
+  g.n = min(n * p.unit, w.row.nblk - off * p.unit);
+  g.whole = n == w.row.units;
+  g.first = !w.begun;
+  w.begun = true;
+  w.unit += n;
+  w.left -= n;
+  return true;
+}
+
+// Few rows (tile_rows 8 or 16) and many (128 or 256). tm_k, tm_v: the whole cache as rows of
+// 64 bytes, a block a box.
 cudaError_t launch_kv8_attend_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
                                    cudaStream_t s);
+cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s);
 cudaError_t configure_kv8_kernels();
 
 // E4M3 pairs (two bytes, low byte first) to and from half and float pairs.

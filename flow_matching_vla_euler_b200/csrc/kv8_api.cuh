@@ -18,7 +18,7 @@ struct vla_kv8 {
 
 namespace {
 
-constexpr int kKv8TileRows = 16;   // query rows of a tile of the few-rows kernel
+constexpr int kKv8TileRows = 16;   // largest tile of query rows, for the workspace
 
 // The cache as rows of 64 bytes, boxes of one block (box_rows rows), 64-byte swizzle.
 int make_tmap_rows64(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
@@ -186,7 +186,7 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   if (dev != h->dev) return fail(VLA_ERR_STATE, "the cache is on device %d, the current device is %d", h->dev, dev);
   if (a->layer < 0 || a->layer >= h->cfg.n_layers)
     return fail(VLA_ERR_SHAPE, "layer %d of %d", a->layer, h->cfg.n_layers);
-  if (a->batch < 1 || a->batch > 65535 || (!a->slots && a->batch > h->cfg.n_slots))
+  if (a->batch < 1 || (!a->slots && a->batch > h->cfg.n_slots))
     return fail(VLA_ERR_SHAPE, "batch %d: at least 1, at most %d slots", a->batch, h->cfg.n_slots);
   if (a->n_heads < 1 || a->n_heads % h->c.n_kv)
     return fail(VLA_ERR_SHAPE, "n_heads %d: a positive multiple of %d K/V heads", a->n_heads, h->c.n_kv);
@@ -227,12 +227,14 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   p.err = h->err;
   p.ws = h->ws;
   p.ws_ml = h->ws_ml;
-  const double tiles = std::ceil(static_cast<double>(a->n_q) * p.group / kKv8TileRows);
-  if (tiles * h->c.n_kv > 65535.0)
-    return fail(VLA_ERR_SHAPE, "%d query tokens of %d heads: at most 65535 tiles of %d rows", a->n_q, a->n_heads,
-                kKv8TileRows);
+  const double rows = static_cast<double>(a->n_q) * p.group;
+  p.tile_rows = rows <= 8 ? 8 : 16;
+  p.unit = 1;
+  const double tiles = std::ceil(rows / p.tile_rows);
+  if (tiles * a->batch > 1073741824.0)
+    return fail(VLA_ERR_SHAPE, "%d rows of %d query tokens and %d heads: too many tiles", a->batch, a->n_q, a->n_heads);
   p.tiles = static_cast<int>(tiles);
-  const double units = tiles * h->c.n_kv * a->batch * h->c.nblk;
+  const double units = tiles * h->c.n_kv * a->batch * cdiv(h->c.nblk, p.unit);
   p.grid = static_cast<int>(std::min(units, static_cast<double>(h->sm_count)));
   CU(launch_kv8_attend_rows(h->tm_k, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
   return VLA_OK;
