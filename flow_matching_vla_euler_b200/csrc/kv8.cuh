@@ -107,52 +107,58 @@ __device__ __forceinline__ void kv8_seen(const Kv8AttendParams& p, const Kv8Tile
   lo = p.window ? max(0, r.pos + i - p.window + 1) : 0;
 }
 
-// Sum over the CTA's threads, the same value in all of them (red: one slot per warp).
-__device__ __forceinline__ long long cta_sum(long long v, long long* red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long s = 0;
-  for (int i = 0; i < static_cast<int>(blockDim.x + 31) / 32; ++i) s += red[i];
-  return s;
-}
-
-__device__ __forceinline__ long long kv8_weight(const Kv8AttendParams& p, int e) {
+// Units of entry e = (batch row, tile), all K/V heads; 0 behind the last entry.
+__device__ __forceinline__ int kv8_weight(const Kv8AttendParams& p, int e) {
   if (e >= p.batch * p.tiles) return 0;
-  return static_cast<long long>(kv8_tile(p, e / p.tiles, e % p.tiles).units) * p.c.n_kv;
+  return kv8_tile(p, e / p.tiles, e % p.tiles).units * p.c.n_kv;
 }
 
-__device__ __forceinline__ long long kv8_total(const Kv8AttendParams& p, long long* red) {
-  long long n = 0;
-  for (int e = threadIdx.x; e < p.batch * p.tiles; e += blockDim.x) n += kv8_weight(p, e);
-  return cta_sum(n, red);
-}
+// The line of units of a call (fewer than 2^31: the host sees to it), as a warp sees it: every
+// warp works it out for itself, up to 128 entries from one round of loads.
+struct Kv8Line {
+  int total, per, rem;
+  int w[4];                       // this lane's entries lane, lane + 32, ... (of the first 128)
+};
 
-__device__ __forceinline__ long long part_begin(long long total, int grid, int c) { return total * c / grid; }
-
-// The (batch row, tile) entry that holds unit u < total, and the unit's number inside it.
-// Every warp of the CTA works it out for itself.
-__device__ __forceinline__ int kv8_find(const Kv8AttendParams& p, long long u, long long* inside) {
+__device__ __forceinline__ Kv8Line kv8_line(const Kv8AttendParams& p) {
+  Kv8Line n;
   const int lane = threadIdx.x & 31;
-  long long at = 0;
-  for (int e = 0;; e += 32) {
-    const long long mine = kv8_weight(p, e + lane);
-    long long inc = mine;
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    n.w[i] = kv8_weight(p, 32 * i + lane);
+    sum += n.w[i];
+  }
+  for (int e = 128 + lane; e < p.batch * p.tiles; e += 32) sum += kv8_weight(p, e);
+  n.total = __reduce_add_sync(0xffffffffu, sum);
+  n.per = n.total / p.grid;
+  n.rem = n.total % p.grid;
+  return n;
+}
+
+// First unit of part c: the parts differ by at most one unit.
+__device__ __forceinline__ int kv8_begin(const Kv8Line& n, int c) { return c * n.per + min(c, n.rem); }
+
+// The entry that holds unit u < total, and the unit's number inside it.
+__device__ __forceinline__ int kv8_find(const Kv8AttendParams& p, const Kv8Line& n, int u, int* inside) {
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  for (int i = 0;; ++i) {
+    const int mine = i == 0 ? n.w[0] : i == 1 ? n.w[1] : i == 2 ? n.w[2] : i == 3 ? n.w[3] : kv8_weight(p, 32 * i + lane);
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
     const unsigned past = __ballot_sync(0xffffffffu, at + inc > u);
     if (past) {
       const int k = __ffs(past) - 1;
       *inside = u - at - __shfl_sync(0xffffffffu, inc - mine, k);
-      return e + k;
+      return 32 * i + k;
     }
     at += __shfl_sync(0xffffffffu, inc, 31);
-    if (e + 32 >= p.batch * p.tiles) {   // u >= total: not reached
+    if (32 * i + 32 >= p.batch * p.tiles) {   // u >= total: not reached
       *inside = 0;
       return 0;
     }
@@ -168,22 +174,21 @@ struct Kv8Segment {
 };
 
 struct Kv8Walk {
-  int e;
-  long long unit, left;
-  Kv8Tile row;
+  int e, unit, left;
   bool begun;
+  Kv8Tile row;
 };
 
-__device__ __forceinline__ Kv8Walk kv8_walk(const Kv8AttendParams& p, long long* red) {
+__device__ __forceinline__ Kv8Walk kv8_walk(const Kv8AttendParams& p) {
   Kv8Walk w;
-  const long long total = kv8_total(p, red);
-  const long long u0 = part_begin(total, p.grid, blockIdx.x);
-  w.left = part_begin(total, p.grid, blockIdx.x + 1) - u0;
+  const Kv8Line n = kv8_line(p);
+  const int u0 = kv8_begin(n, blockIdx.x);
+  w.left = kv8_begin(n, blockIdx.x + 1) - u0;
   w.begun = false;
   w.e = 0;
   w.unit = 0;
   if (w.left) {
-    w.e = kv8_find(p, u0, &w.unit);
+    w.e = kv8_find(p, n, u0, &w.unit);
     w.row = kv8_tile(p, w.e / p.tiles, w.e % p.tiles);
   }
   return w;
@@ -191,17 +196,16 @@ __device__ __forceinline__ Kv8Walk kv8_walk(const Kv8AttendParams& p, long long*
 
 __device__ __forceinline__ bool kv8_next(const Kv8AttendParams& p, Kv8Walk& w, Kv8Segment& g) {
   if (w.left == 0) return false;
-  while (w.unit >= static_cast<long long>(w.row.units) * p.c.n_kv) {
+  while (w.unit >= w.row.units * p.c.n_kv) {
     ++w.e;
     w.unit = 0;
     w.row = kv8_tile(p, w.e / p.tiles, w.e % p.tiles);
   }
-  const int off = static_cast<int>(w.unit % w.row.units);
-  const int n = static_cast<int>(min(static_cast<long long>(w.row.units - off), w.left));
+  const int off = w.unit % w.row.units, n = min(w.row.units - off, w.left);
   g.row = w.row;
   g.b = w.e / p.tiles;
   g.tile = w.e % p.tiles;
-  g.head = static_cast<int>(w.unit / w.row.units);
+  g.head = w.unit / w.row.units;
   g.blk = w.row.blk0 + off * p.unit;
   g.n = min(n * p.unit, w.row.nblk - off * p.unit);
   g.whole = n == w.row.units;

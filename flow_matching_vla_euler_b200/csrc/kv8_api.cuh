@@ -231,10 +231,11 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   p.tile_rows = rows <= 8 ? 8 : 16;
   p.unit = 1;
   const double tiles = std::ceil(rows / p.tile_rows);
-  if (tiles * a->batch > 1073741824.0)
-    return fail(VLA_ERR_SHAPE, "%d rows of %d query tokens and %d heads: too many tiles", a->batch, a->n_q, a->n_heads);
-  p.tiles = static_cast<int>(tiles);
   const double units = tiles * h->c.n_kv * a->batch * cdiv(h->c.nblk, p.unit);
+  if (units > 2147483647.0)
+    return fail(VLA_ERR_SHAPE, "%.0f units of work (tiles of %d query rows times blocks), at most 2^31 - 1 a call", units,
+                p.tile_rows);
+  p.tiles = static_cast<int>(tiles);
   p.grid = static_cast<int>(std::min(units, static_cast<double>(h->sm_count)));
   CU(launch_kv8_attend_rows(h->tm_k, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
   return VLA_OK;

@@ -36,17 +36,18 @@ constexpr int kWarps = 8;                    // consumer warps; warp 8 feeds the
 constexpr int kThreads = 384;
 constexpr int kStageK = 16384;               // K bytes of a stage; V follows
 constexpr int kStage = 2 * kStageK;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr float kMoveBy = 32.0f;             // the reference maximum moves when passed by 2^32
 
 template <int D, int R>
 struct RowsSmem {
   static constexpr int qfrag = D / 32 * 512 * (R / 8);            // A fragments of Q, 16 bytes a lane
   static constexpr int q = kStages * kStage;
-  static constexpr int xch = q + qfrag;                           // [8 warps][R rows][32 columns] fp32
-  static constexpr int ml = xch + kWarps * R * 32 * 4;            // [8 warps][R rows] (maximum, sum)
+  static constexpr int xch = q + qfrag;                           // [8 warps][R rows][columns] fp32
+  static constexpr int cols = D < 1024 / R ? D : 1024 / R;         // columns of a round of the exchange
+  static constexpr int ml = xch + kWarps * R * cols * 4;          // [8 warps][R rows] (maximum, sum)
   static constexpr int misc = ml + kWarps * R * 8;                // row factors, scan
-  static constexpr int scale = misc + 256;                        // [stages][4 blocks] float4
+  static constexpr int scale = misc + 64;                         // [stages][4 blocks] float4
   static constexpr int bar = scale + kStages * 4 * 16;
   static constexpr int total = bar + kStages * 16;
 };
@@ -89,7 +90,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sm = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* rowf = reinterpret_cast<float*>(smem + S::misc);         // [R] score factors
-  long long* red = reinterpret_cast<long long*>(smem + S::misc + 64);
   const uint32_t full0 = sm + S::bar, empty0 = full0 + 8 * kStages;
 
   if (threadIdx.x == 0) {
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
       if (kv8_tile(p, b, 0).slot < 0) report(p.err, kKv8BadRow);
-  Kv8Walk w = kv8_walk(p, red);
+  Kv8Walk w = kv8_walk(p);
   __syncthreads();
 
   Kv8Segment g;
@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * R + gq + 8 * r].x);
       fac[r] = m[r] == -INFINITY ? 1.0f : exp2_approx(m[r] - mm);
     }
-    // this thread's output: row rr, kCols columns of each 32
-    constexpr int kCols = R * 32 / (kWarps * 32);
-    const int rr = threadIdx.x / (32 / kCols), cc = (threadIdx.x % (32 / kCols)) * kCols;
+    // this thread's output: row rr, kCols columns of each round of S::cols
+    constexpr int kCols = R * S::cols / (kWarps * 32);
+    const int rr = threadIdx.x / (S::cols / kCols), cc = (threadIdx.x % (S::cols / kCols)) * kCols;
     float mm = -INFINITY, ll = 0.0f;
     for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * R + rr].x);
     for (int i = 0; i < kWarps; ++i) {
@@ -381,23 +381,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __nv_bfloat16* dst = p.out + g.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
     float* xb = reinterpret_cast<float*>(smem + S::xch);
 #pragma unroll
-    for (int c0 = 0; c0 < D / 32; ++c0) {
+    for (int c0 = 0; c0 < D; c0 += S::cols) {
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj)
+      for (int jj = 0; jj < S::cols / 8; ++jj)
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
-          *reinterpret_cast<float2*>(xb + (warp * R + gq + 8 * r) * 32 + jj * 8 + 2 * t) =
-              make_float2(o[c0 * 4 + jj][2 * r] * fac[r], o[c0 * 4 + jj][2 * r + 1] * fac[r]);
+          *reinterpret_cast<float2*>(xb + (warp * R + gq + 8 * r) * S::cols + jj * 8 + 2 * t) =
+              make_float2(o[c0 / 8 + jj][2 * r] * fac[r], o[c0 / 8 + jj][2 * r + 1] * fac[r]);
       named_bar_sync(1, kWarps * 32);
       if (rr < rows) {
         float v[kCols] = {};
 #pragma unroll
         for (int i = 0; i < kWarps; ++i)
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) v[c] += xb[(i * R + rr) * 32 + cc + c];
+          for (int c = 0; c < kCols; ++c) v[c] += xb[(i * R + rr) * S::cols + cc + c];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          const int d = c0 * 32 + cc + c;
+          const int d = c0 + cc + c;
           if (!g.whole) ws[d] = v[c];
           else if (d < p.c.D) dst[d] = __float2bfloat16_rn(v[c] * norm);
         }
@@ -416,45 +416,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merges the parts of the items that more than one CTA worked on. CTA (x, y) looks at the cut
 // before part y + 1: if it is the first cut inside an item, it merges that item's rows
-// x, x + gridDim.x, ... Ds threads, a column each.
+// x, x + gridDim.x, ... Ds threads, a column each; the parts' weights are found by all threads
+// at once, kMergeParts at a time.
+constexpr int kMergeParts = 64;
 __global__ void kv8_merge_kernel(const Kv8AttendParams p, int ds) {
-  __shared__ long long red[8];
-  const long long total = kv8_total(p, red);
+  __shared__ float2 ml[kMergeParts];
+  __shared__ int at[kMergeParts];
+  const Kv8Line line = kv8_line(p);
+  const int cut = blockIdx.y + 1, uc = kv8_begin(line, cut);
+  int inside = 0, e = 0, u0 = uc, u1 = uc;
+  Kv8Tile row{};
+  if (uc < line.total) {
+    e = kv8_find(p, line, uc, &inside);
+    row = kv8_tile(p, e / p.tiles, e % p.tiles);
+    u0 = uc - inside % row.units;
+    u1 = u0 + row.units;
+  }
   pdl_wait();
-  const int cut = blockIdx.y + 1;
-  const long long uc = part_begin(total, p.grid, cut);
-  if (uc >= total) return;
-  long long inside;
-  const int e = kv8_find(p, uc, &inside);
-  const int b = e / p.tiles, tile = e % p.tiles;
-  const Kv8Tile row = kv8_tile(p, b, tile);
-  const int head = static_cast<int>(inside / row.units);
-  const long long u0 = uc - inside % row.units, u1 = u0 + row.units;
-  // the first cut inside the item (empty parts have their cuts at the same unit)
-  if (uc == u0 || part_begin(total, p.grid, cut - 1) > u0) return;
+  // the first cut inside the item (parts without units have their cuts at the same unit)
+  if (uc == u0 || kv8_begin(line, cut - 1) > u0) return;
+  const int b = e / p.tiles, tile = e % p.tiles, head = inside / row.units;
   const int rows = min(p.tile_rows, row.cnt * p.group - tile * p.tile_rows);
+  int c1 = cut;                                          // parts cut - 1 .. c1 - 1 meet the item
+  if (line.per > 0) c1 = min(p.grid, cut + (u1 - uc - 1) / line.per + 1);
+  while (c1 > cut && kv8_begin(line, c1 - 1) >= u1) --c1;
+  if (line.per == 0) while (c1 < p.grid && kv8_begin(line, c1) < u1) ++c1;
   for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    float mm = -INFINITY;
-    int c1 = cut - 1;
-    for (; c1 < p.grid && part_begin(total, p.grid, c1) < u1; ++c1) {
-      const long long s = part_begin(total, p.grid, c1);
-      if (s == part_begin(total, p.grid, c1 + 1)) continue;   // an empty part
-      mm = fmaxf(mm, p.ws_ml[(2 * c1 + (s >= u0 ? 0 : 1)) * p.tile_rows + r].x);
+    float mm = -INFINITY, ll = 0.0f, v = 0.0f;
+    for (int c0 = cut - 1; c0 < c1; c0 += kMergeParts) {
+      const int n = min(kMergeParts, c1 - c0);
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int s = kv8_begin(line, c0 + i);
+        // the item in which a CTA's range starts is its first; one that starts later, its second
+        at[i] = (2 * (c0 + i) + (s >= u0 ? 0 : 1)) * p.tile_rows + r;
+        ml[i] = s == kv8_begin(line, c0 + i + 1) ? make_float2(-INFINITY, 0.0f) : p.ws_ml[at[i]];
+      }
+      __syncthreads();
+      float nm = mm;
+      for (int i = 0; i < n; ++i) nm = fmaxf(nm, ml[i].x);
+      const float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - nm);
+      mm = nm;
+      ll *= k;
+      v *= k;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float2 y = ml[i];
+        const float x = p.ws[static_cast<size_t>(at[i]) * ds + threadIdx.x];
+        const float f = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - mm);
+        ll = fmaf(y.y, f, ll);
+        if (y.y != 0.0f) v = fmaf(x, f, v);              // (a NaN sum counts)
+      }
     }
-    float ll = 0.0f, v = 0.0f;
-#pragma unroll 4
-    for (int i = cut - 1; i < c1; ++i) {
-      const long long s = part_begin(total, p.grid, i);
-      if (s == part_begin(total, p.grid, i + 1)) continue;
-      // the item in which a CTA's range starts is its first; one that starts later, its second
-      const int slot = (2 * i + (s >= u0 ? 0 : 1)) * p.tile_rows + r;
-      const float2 y = p.ws_ml[slot];
-      const float f = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - mm);
-      ll = fmaf(y.y, f, ll);
-      v = fmaf(p.ws[static_cast<size_t>(slot) * ds + threadIdx.x], f, v);
-    }
-    const int at = tile * p.tile_rows + r;
-    const int qi = at / p.group, qh = head * p.group + at % p.group;
+    const int q = tile * p.tile_rows + r;
+    const int qi = q / p.group, qh = head * p.group + q % p.group;
     if (static_cast<int>(threadIdx.x) < p.c.D)
       p.out[b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2] + threadIdx.x] =
           __float2bfloat16_rn(ll == 0.0f ? 0.0f : v / ll);
