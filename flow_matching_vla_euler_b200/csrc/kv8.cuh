@@ -220,6 +220,10 @@ __device__ __forceinline__ bool kv8_next(const Kv8AttendParams& p, Kv8Walk& w, K
 // 64 bytes, a block a box.
 cudaError_t launch_kv8_attend_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
                                    cudaStream_t s);
+// tm_k here: boxes of 64 rows (one panel of a block).
+cudaError_t launch_kv8_attend_tc(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
+                                 cudaStream_t s);
+cudaError_t configure_kv8_tc_kernels();
 cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s);
 cudaError_t configure_kv8_kernels();
 

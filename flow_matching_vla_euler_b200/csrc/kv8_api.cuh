@@ -13,12 +13,13 @@ struct vla_kv8 {
   float* ws = nullptr;
   float2* ws_ml = nullptr;
   int* err = nullptr;
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k, tm_v, tm_kp;   // a block a box; K by panels of 64 dims
 };
 
 namespace {
 
-constexpr int kKv8TileRows = 16;   // largest tile of query rows, for the workspace
+// Query rows of a tile of the many-rows kernel.
+int kv8_tc_rows(const Kv8Cache& c) { return c.Ds == 256 ? 128 : 256; }
 
 // The cache as rows of 64 bytes, boxes of one block (box_rows rows), 64-byte swizzle.
 int make_tmap_rows64(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
@@ -134,12 +135,14 @@ int vla_kv8_create(const vla_kv8_config* cfg, vla_kv8** out) {
   if ((rc = dalloc(h, &c.k, blocks * c.Ds * 64))) return cleanup(rc);
   if ((rc = dalloc(h, &c.v, blocks * c.Ds * 64))) return cleanup(rc);
   if ((rc = dalloc(h, &c.scale, blocks))) return cleanup(rc);
-  if ((rc = dalloc(h, &h->ws, static_cast<size_t>(2) * sm_count * kKv8TileRows * c.Ds))) return cleanup(rc);
-  if ((rc = dalloc(h, &h->ws_ml, static_cast<size_t>(2) * sm_count * kKv8TileRows))) return cleanup(rc);
+  if ((rc = dalloc(h, &h->ws, static_cast<size_t>(2) * sm_count * kv8_tc_rows(c) * c.Ds))) return cleanup(rc);
+  if ((rc = dalloc(h, &h->ws_ml, static_cast<size_t>(2) * sm_count * kv8_tc_rows(c)))) return cleanup(rc);
   if ((rc = dalloc(h, &h->err, 1))) return cleanup(rc);
   if ((rc = make_tmap_rows64(&h->tm_k, c.k, blocks * c.Ds, c.Ds))) return cleanup(rc);
   if ((rc = make_tmap_rows64(&h->tm_v, c.v, blocks * c.Ds, c.Ds))) return cleanup(rc);
+  if ((rc = make_tmap_rows64(&h->tm_kp, c.k, blocks * c.Ds, 64))) return cleanup(rc);
   CU_CLEANUP(configure_kv8_kernels());
+  CU_CLEANUP(configure_kv8_tc_kernels());
   CU_CLEANUP(launch_kv8_init(c, 0));
   CU_CLEANUP(cudaDeviceSynchronize());
   *out = h;
@@ -228,8 +231,9 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   p.ws = h->ws;
   p.ws_ml = h->ws_ml;
   const double rows = static_cast<double>(a->n_q) * p.group;
-  p.tile_rows = rows <= 8 ? 8 : 16;
-  p.unit = 1;
+  const bool few = rows <= 16;
+  p.tile_rows = rows <= 8 ? 8 : few ? 16 : kv8_tc_rows(h->c);
+  p.unit = few ? 1 : 2;
   const double tiles = std::ceil(rows / p.tile_rows);
   const double units = tiles * h->c.n_kv * a->batch * cdiv(h->c.nblk, p.unit);
   if (units > 2147483647.0)
@@ -237,7 +241,8 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
                 p.tile_rows);
   p.tiles = static_cast<int>(tiles);
   p.grid = static_cast<int>(std::min(units, static_cast<double>(h->sm_count)));
-  CU(launch_kv8_attend_rows(h->tm_k, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
+  if (few) CU(launch_kv8_attend_rows(h->tm_k, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
+  else CU(launch_kv8_attend_tc(h->tm_kp, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
   return VLA_OK;
 }
 

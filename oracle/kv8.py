@@ -91,12 +91,13 @@ class Kv8Model:
                fill=0.0):
         """q: float64 [batch, n_q, H, D]. Returns out (rows behind q_count: `fill`), the natural
         log of the softmax sums and, for error bounds, the weighted mean of |v|, the largest sum
-        of |q_d k_d| of a visible key, and n * the largest softmax weight * V scale of n keys."""
+        of |q_d k_d| of a visible key (mag[0]) and of max |q| |k_d| (mag[1]), and n * the largest
+        softmax weight * V scale of n keys."""
         B, nq, H, D = q.shape
         scale = 1.0 / np.sqrt(D) if scale is None else scale
         out = np.full((B, nq, H, D), fill)
         mean_v = np.zeros((B, nq, H, D))
-        mag = np.zeros((B, nq, H))
+        mag = np.zeros((2, B, nq, H))
         lse = np.full((B, nq, H), -np.inf)
         top = np.zeros((B, nq, H))
         for b in range(B):
@@ -119,7 +120,8 @@ class Kv8Model:
                     e = np.exp(x - m)
                     out[b, i, h] = e @ v[lo:hi] / e.sum()
                     mean_v[b, i, h] = e @ np.abs(v[lo:hi]) / e.sum()
-                    mag[b, i, h] = (np.abs(k[lo:hi]) @ np.abs(q[b, i, h])).max()
+                    mag[0, b, i, h] = (np.abs(k[lo:hi]) @ np.abs(q[b, i, h])).max()
+                    mag[1, b, i, h] = np.abs(k[lo:hi]).sum(1).max() * np.abs(q[b, i, h]).max()
                     lse[b, i, h] = m + np.log(e.sum())
                     top[b, i, h] = (hi - lo) * (e * sv[lo:hi]).max() / e.sum()
         return out, lse, mean_v, mag, top

@@ -7,12 +7,14 @@ E4M3 terms, each off by half a step 2^-4), and the scores' error e_s, both of wh
 through sum p |v| / sum p:
     |err| <= 2^-8 |o| + (2^-8 + 2 e_s) * mean|v| (1 + 2^-7)
                  + 448 * 2^-22 * top + 2^-133
-with e_s = scale * (D + 8) * 2^-23 * max_j sum_d |q_d k_jd| + 2^-20 (fp32 sums of exact
-products, truncated at worst; exp2 and the subtraction of the maximum, 2^-20 in all). The last
-terms are the ends of the number ranges: a weight times its V scale is held relative to the
-largest of the row, which is at least 1, with a smallest step of 2^-21 (E4M3's second term:
-2^-9 / 16 / 256; fp16's is 2^-24), so each of n keys adds at most 2^-22 of that largest times
-448 (top = n * largest weight * V scale); bf16 ends at 2^-133.
+with e_s = scale * ((D + 8) * 2^-23 * max_j sum_d |q_d k_jd| + 2^-17 max|q| max_j sum_d |k_jd|)
++ 2^-20 (fp32 sums of exact products, truncated at worst; Q as two E4M3 terms of a row scaled
+to a largest value in [128, 256), off by at most half of E4M3's smallest step, 2^-10; exp2
+and the subtraction of the maximum, 2^-20 in all). The last terms are the ends of the number
+ranges: a weight times its V scale is held relative to the largest of the row, which is at
+least 1, with a smallest step of 2^-21 (E4M3's second term: 2^-9 / 16 / 256; fp16's is 2^-24),
+so each of n keys adds at most 2^-22 of that largest times 448 (top = n * largest weight * V
+scale); bf16 ends at 2^-133.
 """
 import numpy as np
 import pytest
@@ -84,7 +86,7 @@ class Pair:
         qn, got, ls = self.attend(Q, lens, **kw)
         ref, rls, mean_v, mag, top = self.m.attend(qn, lens, fill=7.0, **kw)
         scale = kw.get("scale") or 1.0 / np.sqrt(self.m.D)
-        es = (scale * (self.m.D + 8) * 2.0 ** -23 * mag + 2.0 ** -20)[..., None]
+        es = (scale * ((self.m.D + 8) * 2.0 ** -23 * mag[0] + 2.0 ** -17 * mag[1]) + 2.0 ** -20)[..., None]
         tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * es) * mean_v * (1 + 2.0 ** -7)
         tol += 448 * 2.0 ** -22 * top[..., None] + 2.0 ** -133
         assert np.array_equal(np.isnan(got), np.isnan(ref))
