@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, kSlices);
+      mbar_init(empty0 + 8 * i, kWarps);
     }
     fence_mbar_init();
     prefetch_tmap(&tm_k);
@@ -223,14 +223,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = it % kStages;
       const int base = (j / kPer) * kSlices;    // the segment's slices go round the warps
       const int sl = (warp - base % kWarps + kWarps) % kWarps;
-      if (sl >= kSlices) continue;
-      if (!ok || !mbar_wait(full0 + 8 * s, (it / kStages) & 1, p.err)) {
-        ok = false;
-        continue;
-      }
+      // every warp waits for every stage and releases it, also one it has no slice of: a warp
+      // that skipped a stage could take the slot's last phase for its next one
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(full0 + 8 * s, (it / kStages) & 1, p.err)) != 0;
       const int bi = sl >> 1, wsl = sl & 1;
       const int tok = (g.blk + j + bi) * kKv8Block + wsl * 32;
-      if (j + bi < g.n && tok < hi_last && tok + 32 > lo_first) {
+      if (ok && sl < kSlices && j + bi < g.n && tok < hi_last && tok + 32 > lo_first) {
         const uint32_t kb = sm + s * kStage + bi * D * 64 + (wsl * 32 + gq) * 64 + 4 * t;
         const uint32_t vb = sm + s * kStage + kStageK + bi * D * 64 + gq * 64 + 4 * t;
         const float4 sc = *reinterpret_cast<const float4*>(smem + S::scale + s * 64 + bi * 16);
@@ -415,13 +413,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merges the parts of the items that more than one CTA worked on. CTA (x, y) looks at the cut
-// before part y + 1: if it is the first cut inside an item, it merges that item's rows
-// x, x + gridDim.x, ... Ds threads, a column each; the parts' weights are found by all threads
-// at once, kMergeParts at a time.
-constexpr int kMergeParts = 64;
-__global__ void kv8_merge_kernel(const Kv8AttendParams p, int ds) {
-  __shared__ float2 ml[kMergeParts];
-  __shared__ int at[kMergeParts];
+// before part y + 1: if it is the first cut inside an item, it merges kMergeWarps / W rows of
+// that item, W warps a row (W = 1 for the many rows of few parts, all for few rows of many
+// parts): each warp sums every W-th part, a lane D / 32 columns, and the W sums are joined in
+// order in shared memory.
+constexpr int kMergeWarps = 8;
+template <int D, int W>
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Kv8AttendParams p) {
+  constexpr int kPl = D / 32 >= 4 ? D / 32 : 4;          // columns a lane, in groups of 4
+  constexpr int kLanes = D / kPl;
+  constexpr int kG = kPl / 4;
+  __shared__ float2 sml[kMergeWarps];
+  __shared__ float4 so[W > 1 ? kMergeWarps : 1][kG][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Kv8Line line = kv8_line(p);
   const int cut = blockIdx.y + 1, uc = kv8_begin(line, cut);
   int inside = 0, e = 0, u0 = uc, u1 = uc;
@@ -437,60 +441,116 @@ __global__ void kv8_merge_kernel(const Kv8AttendParams p, int ds) {
   if (uc == u0 || kv8_begin(line, cut - 1) > u0) return;
   const int b = e / p.tiles, tile = e % p.tiles, head = inside / row.units;
   const int rows = min(p.tile_rows, row.cnt * p.group - tile * p.tile_rows);
-  int c1 = cut;                                          // parts cut - 1 .. c1 - 1 meet the item
-  if (line.per > 0) c1 = min(p.grid, cut + (u1 - uc - 1) / line.per + 1);
+  const int r = blockIdx.x * (kMergeWarps / W) + warp / W, share = warp % W;
+  if (blockIdx.x * (kMergeWarps / W) >= rows) return;
+  // parts cut - 1 .. c1 - 1 meet the item; all have units, as the cuts inside an item differ
+  int c1 = min(p.grid, cut + (line.per > 0 ? (u1 - uc - 1) / line.per + 1 : u1 - uc));
   while (c1 > cut && kv8_begin(line, c1 - 1) >= u1) --c1;
-  if (line.per == 0) while (c1 < p.grid && kv8_begin(line, c1) < u1) ++c1;
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    float mm = -INFINITY, ll = 0.0f, v = 0.0f;
-    for (int c0 = cut - 1; c0 < c1; c0 += kMergeParts) {
-      const int n = min(kMergeParts, c1 - c0);
-      __syncthreads();
-      for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int s = kv8_begin(line, c0 + i);
+  float mm = -INFINITY, ll = 0.0f;
+  float4 v[kG] = {};
+  if (r < rows) {
+    for (int c0 = cut - 1 + share; c0 < c1; c0 += 32 * W) {
+      // 32 parts' maxima and sums at once, a lane each
+      const int c = c0 + lane * W;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      int at = 0;
+      if (c < c1) {
         // the item in which a CTA's range starts is its first; one that starts later, its second
-        at[i] = (2 * (c0 + i) + (s >= u0 ? 0 : 1)) * p.tile_rows + r;
-        ml[i] = s == kv8_begin(line, c0 + i + 1) ? make_float2(-INFINITY, 0.0f) : p.ws_ml[at[i]];
+        at = (2 * c + (kv8_begin(line, c) >= u0 ? 0 : 1)) * p.tile_rows + r;
+        ml = p.ws_ml[at];
       }
-      __syncthreads();
-      float nm = mm;
-      for (int i = 0; i < n; ++i) nm = fmaxf(nm, ml[i].x);
+      float nm = ml.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
+      nm = fmaxf(nm, mm);
       const float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - nm);
       mm = nm;
       ll *= k;
-      v *= k;
-#pragma unroll 8
+#pragma unroll
+      for (int i = 0; i < kG; ++i) v[i] = make_float4(v[i].x * k, v[i].y * k, v[i].z * k, v[i].w * k);
+      const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - mm);
+      const int n = min(32, (c1 - c0 + W - 1) / W);
+#pragma unroll 4
       for (int i = 0; i < n; ++i) {
-        const float2 y = ml[i];
-        const float x = p.ws[static_cast<size_t>(at[i]) * ds + threadIdx.x];
-        const float f = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - mm);
-        ll = fmaf(y.y, f, ll);
-        if (y.y != 0.0f) v = fmaf(x, f, v);              // (a NaN sum counts)
+        const int ai = __shfl_sync(0xffffffffu, at, i);
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        ll = fmaf(__shfl_sync(0xffffffffu, ml.y, i), fi, ll);
+        if (lane < kLanes) {
+          const float4* x = reinterpret_cast<const float4*>(p.ws + static_cast<size_t>(ai) * D) + lane;
+#pragma unroll
+          for (int j = 0; j < kG; ++j) {
+            const float4 y = x[j * kLanes];
+            v[j] = make_float4(fmaf(y.x, fi, v[j].x), fmaf(y.y, fi, v[j].y), fmaf(y.z, fi, v[j].z), fmaf(y.w, fi, v[j].w));
+          }
+        }
       }
     }
-    const int q = tile * p.tile_rows + r;
-    const int qi = q / p.group, qh = head * p.group + q % p.group;
-    if (static_cast<int>(threadIdx.x) < p.c.D)
-      p.out[b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2] + threadIdx.x] =
-          __float2bfloat16_rn(ll == 0.0f ? 0.0f : v / ll);
-    if (threadIdx.x == 0 && p.lse)
-      p.lse[(static_cast<size_t>(b) * p.n_q + qi) * p.n_heads + qh] =
-          ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
   }
+  if (W > 1) {
+    if (lane == 0) sml[warp] = make_float2(mm, ll);
+#pragma unroll
+    for (int j = 0; j < kG; ++j) so[W > 1 ? warp : 0][j][lane] = v[j];
+    __syncthreads();
+    if (share != 0 || r >= rows) return;
+    float m0 = mm;
+    for (int i = 1; i < W; ++i) m0 = fmaxf(m0, sml[warp + i].x);
+    float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - m0);
+    ll *= k;
+#pragma unroll
+    for (int j = 0; j < kG; ++j) v[j] = make_float4(v[j].x * k, v[j].y * k, v[j].z * k, v[j].w * k);
+    for (int i = 1; i < W; ++i) {
+      const float2 y = sml[warp + i];
+      k = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - m0);
+      ll = fmaf(y.y, k, ll);
+#pragma unroll
+      for (int j = 0; j < kG; ++j) {
+        const float4 z = so[W > 1 ? warp + i : 0][j][lane];
+        v[j] = make_float4(fmaf(z.x, k, v[j].x), fmaf(z.y, k, v[j].y), fmaf(z.z, k, v[j].z), fmaf(z.w, k, v[j].w));
+      }
+    }
+    mm = m0;
+  }
+  if (r >= rows) return;
+  const int q = tile * p.tile_rows + r;
+  const int qi = q / p.group, qh = head * p.group + q % p.group;
+  const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
+  __nv_bfloat16* dst = p.out + b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
+  if (lane < kLanes)
+#pragma unroll
+    for (int j = 0; j < kG; ++j) {
+      const int d = (j * kLanes + lane) * 4;
+      if (d < p.c.D) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[j].x * norm, v[j].y * norm);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(v[j].z * norm, v[j].w * norm);
+        *reinterpret_cast<uint2*>(dst + d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      }
+    }
+  if (lane == 0 && p.lse)
+    p.lse[(static_cast<size_t>(b) * p.n_q + qi) * p.n_heads + qh] =
+        ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
-cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
-  if (p.grid < 2) return cudaSuccess;
+template <int D, int W>
+static cudaError_t launch_merge(const Kv8AttendParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.tile_rows <= 16 ? p.tile_rows : 32, p.grid - 1);
-  cfg.blockDim = dim3(p.c.Ds);
+  cfg.gridDim = dim3((p.tile_rows + kMergeWarps / W - 1) / (kMergeWarps / W), p.grid - 1);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel, p, p.c.Ds);
+  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, W>, p);
+}
+
+cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
+  if (p.grid < 2) return cudaSuccess;
+  const bool few = p.tile_rows <= 16;
+  if (p.c.Ds == 64) return few ? launch_merge<64, 8>(p, s) : launch_merge<64, 1>(p, s);
+  if (p.c.Ds == 128) return few ? launch_merge<128, 8>(p, s) : launch_merge<128, 1>(p, s);
+  return few ? launch_merge<256, 8>(p, s) : launch_merge<256, 1>(p, s);
 }
 
 template <int D, int R>

@@ -58,33 +58,55 @@ struct Tc {
   static constexpr int o_col = 256;                      // tensor memory: S 0 and 128, O from 256
 };
 
-// 64-byte swizzled K-major operand: rows of 64 bytes, 8-row groups 512 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
-  d |= static_cast<uint64_t>(1) << 16;
-  d |= static_cast<uint64_t>(512 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(4) << 61;
-  return d;
+// Operand descriptors in two words. Low: start address >> 4 and leading offset (unused, 1);
+// high: stride between 8-row groups >> 4, version 1, swizzle. K-major rows of 64 bytes (64-byte
+// swizzle, groups 512 bytes apart) and of 128 bytes (128-byte swizzle, 1024).
+constexpr uint32_t kDescSw64 = (512 >> 4) | (1u << 14) | (4u << 29);
+constexpr uint32_t kDescSw128 = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFF) >> 4) | (1u << 16); }
+
+// One lane of a converged warp: 1 in it, 0 in the others. The products are issued by the whole
+// warp under this predicate, so that their operands stay in uniform registers (issued from a
+// branch of one lane, a product took 110 to 190 clocks, here the tensor pipe's own time).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r;
 }
+// The same value in every lane, as one the compiler knows to be uniform.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 // E4M3 x E4M3 (kind::f8f6f4) and fp16 x fp16 (kind::f16): format fields 0, fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_fmt0(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_f8(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
-      "r"(acc)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %0, 0;\n\tmov.b64 a, {%2, %6};\n\tmov.b64 b, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%1], a, b, %4, p;\n\t}\n" ::"r"(lead), "r"(d_tmem), "r"(a_lo),
+      "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescSw64)
       : "memory");
 }
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                            uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc),
-      "r"(acc)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %0, 0;\n\tmov.b64 b, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n\t}\n" ::"r"(lead), "r"(d_tmem), "r"(a_tmem),
+      "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescSw128)
       : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(lead), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // 32 columns of this warp's 32 lanes; the caller waits (tmem_wait_ld).
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
@@ -115,7 +137,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // A segment's units and how the lanes share them.
 struct Plan {
-  int units, steps;      // steps: (lane, unit) pairs in the order the tensor pipe takes them
+  int units;
   bool tiles;            // lane = query tile (else: lane = every second unit, or S buffer)
 };
 template <int D>
@@ -123,7 +145,6 @@ __device__ __forceinline__ Plan make_plan(const Kv8AttendParams& p, const Kv8Seg
   Plan r;
   r.units = (g.n + 1) / 2;
   r.tiles = Tc<D>::two && g.row.cnt * p.group - g.tile * Tc<D>::rows > 128;
-  r.steps = r.tiles ? 2 * r.units : r.units;
   return r;
 }
 
@@ -139,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t kfull = sm + S::bar, kempty = kfull + 8 * S::nk;
   const uint32_t rfull = kempty + 8 * S::nk, rempty = rfull + 8 * S::nv;      // V as stored
   const uint32_t vfull = rempty + 8 * S::nv, vempty = vfull + 8 * S::nv;      // V widened
-  const uint32_t sfull = vempty + 8 * S::nv, pfull = sfull + 16, odone = pfull + 16, qfull = odone + 16;
+  const uint32_t sfull = vempty + 8 * S::nv, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 16;   // pfull: [lane][block]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::bar + 504);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -156,7 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + 8 * i, 1);
-      mbar_init(pfull + 8 * i, S::two ? 4 : 8);
+      mbar_init(pfull + 16 * i, 4);
+      mbar_init(pfull + 16 * i + 8, 4);
       mbar_init(odone + 8 * i, 1);
     }
     mbar_init(qfull, 8);
@@ -215,51 +237,105 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no copies left in flight
       for (int i = kt > S::nk ? kt - S::nk : 0; i < kt; ++i) mbar_wait(kfull + 8 * (i % S::nk), (i / S::nk) & 1, p.err);
       for (int i = vt > S::nv ? vt - S::nv : 0; i < vt; ++i) mbar_wait(rfull + 8 * (i % S::nv), (i / S::nv) & 1, p.err);
-    } else if (warp == 1 && lane == 0) {
-      // ---- products
+    } else if (warp == 1) {
+      // ---- products, by the converged warp. All that can wait before P arrives is done before:
+      // once per unit the V blocks, the next unit's K and the operands' words
+      const uint32_t lead = elect_one();
+      // the warp stays together when a wait gives up
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err)) != 0;
+      };
       constexpr uint32_t id_s = idesc_fmt0(128, kKeys), id_o = idesc_fmt0(128, D);
-      int kt = 0, vt = 0, seg = 0, done[2] = {0, 0};      // units and blocks used, steps of each lane
+      const uint32_t tm = uniform(tmem), q0 = uniform(desc_lo(sm + S::q));
+      int ks = 0, vs = 0;                                 // next K stage and V block of the rings
+      uint32_t kph = 0, vph = 0, qph = 0, pph = 0;        // phases; pph: bit i of lane i
+      // scores of lane i: query tile at a0, K stage at b0
+      auto scores = [&](int i, uint32_t a0, uint32_t b0) {
+        if (!ok) return;
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            umma_f8(lead, tm + i * 128, a0 + ((term * S::q_half + (kk >> 1) * 8192) >> 4) + 2 * (kk & 1),
+                    b0 + (((kk >> 1) * 8192) >> 4) + 2 * (kk & 1), id_s, (term | kk) != 0 ? 1u : 0u);
+        umma_commit_if(lead, sfull + 8 * i);
+      };
+      // output of lane i: += P V over the unit's one or two blocks at b[]
+      // (the blocks are free after it when `ve` is given; no commit follows the output's own, for
+      // which the CTA waits before it ends)
+      auto output = [&](int i, int n, const uint32_t (&b)[2], uint32_t acc, const uint32_t* ve) {
+        const uint32_t d0 = tm + S::o_col + (S::two ? i * D : 0), a0 = tm + i * 128;
+        wait_all(pfull + 16 * i, (pph >> i) & 1);
+        tc_fence_after();
+        if (ok)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f16_ts(lead, d0, a0 + kk * 8, b[0] + 2 * kk, id_o, kk == 0 ? acc : 1u);
+        wait_all(pfull + 16 * i + 8, (pph >> i) & 1);
+        tc_fence_after();
+        if (ok && n == 2)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f16_ts(lead, d0, a0 + 32 + kk * 8, b[1] + 2 * kk, id_o, 1u);
+        if (ok && ve) umma_commit_if(lead, ve[0]);
+        if (ok && ve && n == 2) umma_commit_if(lead, ve[1]);
+        if (ok) umma_commit_if(lead, odone + 8 * i);
+        pph ^= 1u << i;
+      };
+      auto next_k = [&](uint32_t& b0, uint32_t& empty) {
+        wait_all(kfull + 8 * ks, kph);
+        b0 = uniform(desc_lo(sm + S::k + ks * D * kKeys));
+        empty = kempty + 8 * ks;
+        if (++ks == S::nk) {
+          ks = 0;
+          kph ^= 1;
+        }
+      };
       while (ok && kv8_next(p, w, g)) {
         const Plan pl = make_plan<D>(p, g);
-        ok = mbar_wait(qfull, seg & 1, p.err);
-        ++seg;
-        auto scores = [&](int t) {
-          const int i = t & 1, u = pl.tiles ? t >> 1 : t, s = (kt + u) % S::nk;
-          if (!mbar_wait(kfull + 8 * s, ((kt + u) / S::nk) & 1, p.err)) return false;
-          tc_fence_after();
-          const uint32_t a0 = sm + S::q + (pl.tiles ? i * 2 * S::q_half : 0), b0 = sm + S::k + s * D * kKeys;
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              umma_f8(tmem + i * 128, sdesc_k_sw64(a0 + term * S::q_half + (kk >> 1) * 8192) + 2 * (kk & 1),
-                      sdesc_k_sw64(b0 + (kk >> 1) * 8192) + 2 * (kk & 1), id_s, (term | kk) != 0 ? 1u : 0u);
-          umma_commit(sfull + 8 * i);
-          if (!pl.tiles || i == 1) umma_commit(kempty + 8 * s);
-          return true;
-        };
-        for (int t = 0; t < 2 && t < pl.steps && ok; ++t) ok = scores(t);
-        for (int t = 0; t < pl.steps && ok; ++t) {
-          const int i = t & 1, u = pl.tiles ? t >> 1 : t, n = min(2, g.n - 2 * u);
-          const int oc = S::two ? S::o_col + i * D : S::o_col;
-          const bool first = S::two ? (pl.tiles ? u == 0 : t < 2) : t == 0;
-          if (!(ok = mbar_wait(pfull + 8 * i, done[i] & 1, p.err))) break;
-          ++done[i];
-          for (int c = 0; c < n && ok; ++c) {
-            const int v = vt + 2 * u + c, r = v % S::nv;
-            if (!(ok = mbar_wait(vfull + 8 * r, (v / S::nv) & 1, p.err))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ts(tmem + oc, tmem + i * 128 + c * 32 + kk * 8,
-                          sdesc_k_sw128(sm + S::v16 + r * D * 128) + 2 * kk, id_o, (first && c == 0 && kk == 0) ? 0u : 1u);
-            if (!pl.tiles || i == 1) umma_commit(vempty + 8 * r);
-          }
-          umma_commit(odone + 8 * i);
-          if (t + 2 < pl.steps && ok) ok = scores(t + 2);
+        constexpr uint32_t kTile = (2 * S::q_half) >> 4;  // from one query tile to the next
+        wait_all(qfull, qph);
+        qph ^= 1;
+        tc_fence_after();
+        uint32_t kb = 0, ke = 0;
+        next_k(kb, ke);
+        scores(0, q0, kb);
+        if (pl.tiles) {
+          scores(1, q0 + kTile, kb);
+        } else if (pl.units > 1) {
+          if (ok) umma_commit_if(lead, ke);
+          next_k(kb, ke);
+          scores(1, q0, kb);
         }
-        kt += pl.units;
-        vt += g.n;
+        if (ok) umma_commit_if(lead, ke);
+        for (int u = 0; u < pl.units && ok; ++u) {
+          const int n = min(2, g.n - 2 * u);
+          uint32_t vb[2] = {0, 0}, ve[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (c < n) {
+              wait_all(vfull + 8 * vs, vph);
+              vb[c] = uniform(desc_lo(sm + S::v16 + vs * D * 128));
+              ve[c] = vempty + 8 * vs;
+              if (++vs == S::nv) {
+                vs = 0;
+                vph ^= 1;
+              }
+            }
+          const bool more = u + (pl.tiles ? 1 : 2) < pl.units;
+          if (more) next_k(kb, ke);
+          if (pl.tiles) {
+            const uint32_t acc = u == 0 ? 0u : 1u;
+            output(0, n, vb, acc, nullptr);
+            if (more) scores(0, q0, kb);
+            output(1, n, vb, acc, ve);
+            if (more) scores(1, q0 + kTile, kb);
+          } else {
+            const int i = u & 1;
+            const uint32_t acc = u < (S::two ? 2 : 1) ? 0u : 1u;
+            output(i, n, vb, acc, ve);
+            if (more) scores(i, q0, kb);
+          }
+          if (ok && more) umma_commit_if(lead, ke);
+        }
       }
     }
     __syncwarp();
@@ -419,6 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_scales(min(u + u_step, pl.units - 1));
         const int key0 = (g.blk + 2 * u) * kKv8Block + (S::two ? 0 : grp * 64);
         tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) asm volatile("" : "+f"(x[c]));   // not used before the wait
         if (key0 < lo_last || key0 + kCols > hi_first) {
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
@@ -429,12 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kCols / 64; ++i) {
           float h[4] = {x[64 * i], x[64 * i + 1], x[64 * i + 2], x[64 * i + 3]};
 #pragma unroll
-          for (int c = 4; c < 64; c += 4) {
-            h[0] = fmaxf(h[0], x[64 * i + c]);
-            h[1] = fmaxf(h[1], x[64 * i + c + 1]);
-            h[2] = fmaxf(h[2], x[64 * i + c + 2]);
-            h[3] = fmaxf(h[3], x[64 * i + c + 3]);
-          }
+          for (int c = 4; c < 60; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = max3(h[k], x[64 * i + c + k], x[64 * i + c + 4 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = fmaxf(h[k], x[64 * i + 60 + k]);
           mx = fmaxf(mx, fmaf(fmaxf(fmaxf(h[0], h[1]), fmaxf(h[2], h[3])), gk[i], fv[i]));
         }
         if (!S::two) {                                    // the row's maximum over both halves
@@ -484,12 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           l = fmaf(s0 + s1, un[i], l);
-          tmem_st32_async(tl + buf * 128 + (S::two ? i : grp) * 32, pk);
+          const int blk = S::two ? i : grp;
+          tmem_st32_async(tl + buf * 128 + blk * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull + 16 * buf + 8 * blk);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull + 8 * buf);
         ++step[buf];
       }
 

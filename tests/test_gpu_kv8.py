@@ -377,6 +377,41 @@ def test_a_call_gives_the_same_bits_again_and_on_another_stream(nq):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("D,kv,B,H", [(128, 2, 1, 8), (256, 1, 3, 8), (256, 1, 1, 16), (64, 4, 2, 8)])
+def test_long_rows_from_a_cold_cache(D, kv, B, H):
+    """Slow loads (every line evicted before the call) over many stages of the ring: the warps
+    that share it must not overtake a stage they have no part of."""
+    n = 60001
+    rng = torch.Generator(device="cuda").manual_seed(D + H)
+    c = V.KVCache8(n_layers=1, n_kv_heads=kv, head_dim=D, capacity=n, n_slots=B)
+    x = torch.randn((1, B, n, kv * D), generator=rng, device="cuda").to(torch.bfloat16)
+    c.write(x, x)
+    q = torch.randn((B, 1, H, D), generator=rng, device="cuda").to(torch.bfloat16)
+    lens = i32([n - 7 * b for b in range(B)])
+    first = c.attend(q, lens)
+    out = torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.attend(q, lens, out=out)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        flush.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    c.status()
+    del g
+    k = c.read(n, batch=B)[0].view(torch.bfloat16)[0].view(B, n, kv, D)
+    for b in range(B):
+        m = int(lens[b])
+        kb = k[b, :m].double().repeat_interleave(H // kv, dim=1)
+        w = torch.softmax(torch.einsum("hd,nhd->hn", q[b, 0].double(), kb) / D ** 0.5, dim=1)
+        ref = torch.einsum("hn,nhd->hd", w, kb)
+        mean = torch.einsum("hn,nhd->hd", w, kb.abs())
+        # the bound above with 2 e_s below 1.5e-3 (|q . k| of normal values)
+        assert torch.all((first[b, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7.5 * mean)
+
+
 def test_tensors_of_the_host_and_wrong_types_are_refused():
     c = V.KVCache8(n_layers=1, n_kv_heads=1, head_dim=64, capacity=64, n_slots=2)
     k = torch.zeros((1, 2, 4, 64), dtype=torch.bfloat16, device="cuda")
