@@ -3,24 +3,25 @@
 // Layout. For each (layer, slot, K/V head) the tokens are kept in blocks of 64. A block of K
 // and a block of V are Ds rows of 64 bytes each (Ds = head_dim, at least 64), E4M3:
 //   K  row p * 64 + i, byte c    = token i, dim 64 p + c          (panels of 64 dims)
-//   V  row d, byte 16 w + pos    = dim d, token 16 w + tok(pos)   (transposed)
-// with tok(4t + 2h + e) = 8h + 2t + e (t < 4, h, e < 2): the four tokens that one lane of a
-// 16 x 8 x 16 matrix instruction needs of a 16-token group are one 32-bit word. Both block
-// kinds are one TMA box of Ds rows x 64 bytes under the 64-byte swizzle, which is also the
-// K-major operand layout of tcgen05.mma, and a 32-bit read of 8 rows x 4 words of one chunk
-// touches all 32 banks.
+//   V  row d, byte pos           = dim d, token tok(pos)          (transposed)
+// with tok(16t + 4w + 2h + e) = 16w + 8h + 2t + e (t, w < 4; h, e < 2): the sixteen tokens that
+// one lane of a matrix instruction needs of a row are one 16-byte chunk. Chunk c of row r stands
+// at chunk c ^ ((r >> 1) & 3) of its row: the 64-byte swizzle of tcgen05.mma's K-major operands.
+// So a block, or several in a row, comes to shared memory ready for use by one plain bulk copy.
 // Scales: float4 (K scale, V scale, 0, 0) per block, powers of two, value = scale * e4m3.
 // V never holds the E4M3 NaN: a token whose K or V row is not finite has a K row of NaN and
 // a V row of zeros, so that a weight of zero makes a stored token count for nothing.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace vla {
+
+// Byte of chunk c (16 bytes) of row r of a block.
+__host__ __device__ constexpr int kv8_chunk(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
 
 constexpr int kKv8Block = 64;        // tokens per block
 constexpr int kKv8MinExp = -60;      // smallest scale 2^-60
@@ -31,6 +32,24 @@ struct Kv8Cache {
   uint8_t* v;
   float4* scale;       // [L][slots][n_kv][nblk]
   int n_layers, n_slots, n_kv, nblk, capacity, D, Ds;
+};
+
+// n / d for 0 <= n < 2^31 and a divisor d >= 1 fixed on the host: with 2^s >= d and
+// m = ceil(2^(32 + s) / d) - 2^32, the quotient is (mulhi(n, m) + n) >> s.
+struct FastDiv {
+  uint32_t mul, shift;
+  int d;
+  FastDiv() = default;
+  explicit FastDiv(int div) : d(div) {
+    shift = 0;
+    while ((1ull << shift) < static_cast<unsigned long long>(div)) ++shift;
+    const unsigned long long m = ((1ull << shift) - static_cast<unsigned>(div)) << 32;
+    mul = static_cast<uint32_t>((m + static_cast<unsigned>(div) - 1) / static_cast<unsigned>(div));
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * d; }
 };
 
 // Rows of a write or a read: row b holds tokens pos[b] .. pos[b] + count[b] - 1 of slots[b]
@@ -56,10 +75,10 @@ struct Kv8AttendParams {
   long long q_st[3], o_st[3];          // element strides: batch, token, head
   const int *slots, *kv_len, *q_pos, *q_count;   // slots, q_pos, q_count may be null
   int layer, batch, n_q, n_heads, group;         // group = n_heads / n_kv
+  FastDiv by_group, by_tiles;
   int causal, window;
   float scale_log2;                    // softmax scale * log2(e)
   int tile_rows, tiles;                // query rows of a tile, tiles of a (row, K/V head)
-  int unit;                            // blocks of 64 tokens in a unit of work
   float* ws;                           // partial outputs [2 * CTAs][tile_rows][Ds]
   float2* ws_ml;                       // [2 * CTAs][tile_rows] (reference maximum, sum)
   int grid;                            // CTAs of the attention kernel
@@ -67,14 +86,14 @@ struct Kv8AttendParams {
 };
 
 // ---- the division of the work
-// An item is a tile of query rows of one (batch row, K/V head), its units the blocks that any
-// of its queries can see. All units stand in a line (batch row, tile, K/V head, block); CTA c
+// An item is a tile of query rows of one (batch row, K/V head), its units the blocks of 64
+// tokens that any of its queries can see. All units stand in a line (batch row, tile, K/V head, block); CTA c
 // of `grid` takes the units [total * c / grid, total * (c + 1) / grid). So the CTAs have equal
 // work for any lengths, and at most two of a CTA's items are shared with others.
 
 struct Kv8Tile {
   int slot, len, pos, cnt;             // slot < 0: refused, nothing of the row is written
-  int blk0, nblk, units;               // units 0: no queries in this tile
+  int blk0, units;                     // blocks any of its queries can see; units 0: no queries
 };
 
 __device__ __forceinline__ Kv8Tile kv8_tile(const Kv8AttendParams& p, int b, int tile) {
@@ -83,21 +102,20 @@ __device__ __forceinline__ Kv8Tile kv8_tile(const Kv8AttendParams& p, int b, int
   r.len = p.kv_len[b];
   r.cnt = p.q_count ? p.q_count[b] : p.n_q;
   r.pos = p.q_pos ? p.q_pos[b] : r.len - r.cnt;
-  r.blk0 = r.nblk = r.units = 0;
+  r.blk0 = r.units = 0;
   if (r.slot < 0 || r.slot >= p.c.n_slots || r.len < 0 || r.len > p.c.capacity || r.cnt < 0 || r.cnt > p.n_q ||
       r.pos < -p.n_q || r.pos > p.c.capacity) {
     r.slot = -1;
     r.cnt = 0;
     return r;
   }
-  const int i0 = tile * p.tile_rows / p.group;
+  const int i0 = p.by_group.div(tile * p.tile_rows);
   if (i0 >= r.cnt) return r;
-  const int i1 = min(r.cnt - 1, ((tile + 1) * p.tile_rows - 1) / p.group);
+  const int i1 = min(r.cnt - 1, p.by_group.div((tile + 1) * p.tile_rows - 1));
   const int hi = p.causal ? min(r.len, r.pos + i1 + 1) : r.len;
   const int lo = p.window ? max(0, r.pos + i0 - p.window + 1) : 0;
   r.blk0 = min(lo / kKv8Block, p.c.nblk - 1);
-  r.nblk = max(1, (hi + kKv8Block - 1) / kKv8Block - r.blk0);   // one block even if no key is seen
-  r.units = (r.nblk + p.unit - 1) / p.unit;
+  r.units = max(1, (hi + kKv8Block - 1) / kKv8Block - r.blk0);   // one block even if no key is seen
   return r;
 }
 
@@ -110,7 +128,7 @@ __device__ __forceinline__ void kv8_seen(const Kv8AttendParams& p, const Kv8Tile
 // Units of entry e = (batch row, tile), all K/V heads; 0 behind the last entry.
 __device__ __forceinline__ int kv8_weight(const Kv8AttendParams& p, int e) {
   if (e >= p.batch * p.tiles) return 0;
-  return kv8_tile(p, e / p.tiles, e % p.tiles).units * p.c.n_kv;
+  return kv8_tile(p, p.by_tiles.div(e), p.by_tiles.mod(e)).units * p.c.n_kv;
 }
 
 // The line of units of a call (fewer than 2^31: the host sees to it), as a warp sees it: every
@@ -129,6 +147,7 @@ __device__ __forceinline__ Kv8Line kv8_line(const Kv8AttendParams& p) {
     n.w[i] = kv8_weight(p, 32 * i + lane);
     sum += n.w[i];
   }
+#pragma unroll 1
   for (int e = 128 + lane; e < p.batch * p.tiles; e += 32) sum += kv8_weight(p, e);
   n.total = __reduce_add_sync(0xffffffffu, sum);
   n.per = n.total / p.grid;
@@ -143,6 +162,7 @@ __device__ __forceinline__ int kv8_begin(const Kv8Line& n, int c) { return c * n
 __device__ __forceinline__ int kv8_find(const Kv8AttendParams& p, const Kv8Line& n, int u, int* inside) {
   const int lane = threadIdx.x & 31;
   int at = 0;
+#pragma unroll 1
   for (int i = 0;; ++i) {
     const int mine = i == 0 ? n.w[0] : i == 1 ? n.w[1] : i == 2 ? n.w[2] : i == 3 ? n.w[3] : kv8_weight(p, 32 * i + lane);
     int inc = mine;
@@ -189,25 +209,32 @@ __device__ __forceinline__ Kv8Walk kv8_walk(const Kv8AttendParams& p) {
   w.unit = 0;
   if (w.left) {
     w.e = kv8_find(p, n, u0, &w.unit);
-    w.row = kv8_tile(p, w.e / p.tiles, w.e % p.tiles);
+    w.row = kv8_tile(p, p.by_tiles.div(w.e), p.by_tiles.mod(w.e));
   }
   return w;
 }
 
 __device__ __forceinline__ bool kv8_next(const Kv8AttendParams& p, Kv8Walk& w, Kv8Segment& g) {
   if (w.left == 0) return false;
+#pragma unroll 1
   while (w.unit >= w.row.units * p.c.n_kv) {
     ++w.e;
     w.unit = 0;
-    w.row = kv8_tile(p, w.e / p.tiles, w.e % p.tiles);
+    w.row = kv8_tile(p, p.by_tiles.div(w.e), p.by_tiles.mod(w.e));
   }
-  const int off = w.unit % w.row.units, n = min(w.row.units - off, w.left);
+  g.head = 0;                     // (a few K/V heads: subtraction is shorter than division)
+  int off = w.unit;
+#pragma unroll 1
+  while (off >= w.row.units) {
+    off -= w.row.units;
+    ++g.head;
+  }
+  const int n = min(w.row.units - off, w.left);
   g.row = w.row;
-  g.b = w.e / p.tiles;
-  g.tile = w.e % p.tiles;
-  g.head = w.unit / w.row.units;
-  g.blk = w.row.blk0 + off * p.unit;
-  g.n = min(n * p.unit, w.row.nblk - off * p.unit);
+  g.b = p.by_tiles.div(w.e);
+  g.tile = w.e - g.b * p.tiles;
+  g.blk = w.row.blk0 + off;
+  g.n = n;
   g.whole = n == w.row.units;
   g.first = !w.begun;
   w.begun = true;
@@ -216,13 +243,9 @@ __device__ __forceinline__ bool kv8_next(const Kv8AttendParams& p, Kv8Walk& w, K
   return true;
 }
 
-// Few rows (tile_rows 8 or 16) and many (128 or 256). tm_k, tm_v: the whole cache as rows of
-// 64 bytes, a block a box.
-cudaError_t launch_kv8_attend_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
-                                   cudaStream_t s);
-// tm_k here: boxes of 64 rows (one panel of a block).
-cudaError_t launch_kv8_attend_tc(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
-                                 cudaStream_t s);
+// Few rows (tile_rows 8 or 16) and many (128 or 256).
+cudaError_t launch_kv8_attend_rows(const Kv8AttendParams& p, cudaStream_t s);
+cudaError_t launch_kv8_attend_tc(const Kv8AttendParams& p, cudaStream_t s);
 cudaError_t configure_kv8_tc_kernels();
 cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s);
 cudaError_t configure_kv8_kernels();

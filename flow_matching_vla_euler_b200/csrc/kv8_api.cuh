@@ -13,30 +13,12 @@ struct vla_kv8 {
   float* ws = nullptr;
   float2* ws_ml = nullptr;
   int* err = nullptr;
-  CUtensorMap tm_k, tm_v, tm_kp;   // a block a box; K by panels of 64 dims
 };
 
 namespace {
 
 // Query rows of a tile of the many-rows kernel.
 int kv8_tc_rows(const Kv8Cache& c) { return c.Ds == 256 ? 128 : 256; }
-
-// The cache as rows of 64 bytes, boxes of one block (box_rows rows), 64-byte swizzle.
-int make_tmap_rows64(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
-  auto enc = get_encode();
-  if (!enc) return fail(VLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t dims[2] = {64, rows};
-  cuuint64_t strides[1] = {64};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail(VLA_ERR_CUDA, "cuTensorMapEncodeTiled (K/V blocks) failed (%d) for %llu rows", static_cast<int>(r),
-                static_cast<unsigned long long>(rows));
-  return VLA_OK;
-}
 
 int kv8_validate(const vla_kv8_config* c) {
   if (!c) return fail(VLA_ERR_ARG, "null config");
@@ -46,11 +28,9 @@ int kv8_validate(const vla_kv8_config* c) {
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
     return fail(VLA_ERR_SHAPE, "head_dim %d: 32, 64, 128 or 256", c->head_dim);
   if (c->capacity > (1 << 30)) return fail(VLA_ERR_SHAPE, "capacity %d: at most 2^30 tokens", c->capacity);
-  const double ds = c->head_dim < 64 ? 64 : c->head_dim;
-  const double rows = static_cast<double>(c->n_layers) * c->n_slots * c->n_kv_heads *
-                      ((c->capacity + kKv8Block - 1) / kKv8Block) * ds;
-  if (rows > 2147483647.0)
-    return fail(VLA_ERR_SHAPE, "the cache has %.0f rows of 64 bytes, at most 2^31 - 1 (128 GiB of K) fit", rows);
+  const double blocks = static_cast<double>(c->n_layers) * c->n_slots * c->n_kv_heads *
+                        ((c->capacity + kKv8Block - 1) / kKv8Block);
+  if (blocks > 2147483647.0) return fail(VLA_ERR_SHAPE, "%.0f blocks of 64 tokens, at most 2^31 - 1", blocks);
   return VLA_OK;
 }
 
@@ -138,9 +118,6 @@ int vla_kv8_create(const vla_kv8_config* cfg, vla_kv8** out) {
   if ((rc = dalloc(h, &h->ws, static_cast<size_t>(2) * sm_count * kv8_tc_rows(c) * c.Ds))) return cleanup(rc);
   if ((rc = dalloc(h, &h->ws_ml, static_cast<size_t>(2) * sm_count * kv8_tc_rows(c)))) return cleanup(rc);
   if ((rc = dalloc(h, &h->err, 1))) return cleanup(rc);
-  if ((rc = make_tmap_rows64(&h->tm_k, c.k, blocks * c.Ds, c.Ds))) return cleanup(rc);
-  if ((rc = make_tmap_rows64(&h->tm_v, c.v, blocks * c.Ds, c.Ds))) return cleanup(rc);
-  if ((rc = make_tmap_rows64(&h->tm_kp, c.k, blocks * c.Ds, 64))) return cleanup(rc);
   CU_CLEANUP(configure_kv8_kernels());
   CU_CLEANUP(configure_kv8_tc_kernels());
   CU_CLEANUP(launch_kv8_init(c, 0));
@@ -233,16 +210,17 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   const double rows = static_cast<double>(a->n_q) * p.group;
   const bool few = rows <= 16;
   p.tile_rows = rows <= 8 ? 8 : few ? 16 : kv8_tc_rows(h->c);
-  p.unit = few ? 1 : 2;
   const double tiles = std::ceil(rows / p.tile_rows);
-  const double units = tiles * h->c.n_kv * a->batch * cdiv(h->c.nblk, p.unit);
+  const double units = tiles * h->c.n_kv * a->batch * h->c.nblk;
   if (units > 2147483647.0)
     return fail(VLA_ERR_SHAPE, "%.0f units of work (tiles of %d query rows times blocks), at most 2^31 - 1 a call", units,
                 p.tile_rows);
   p.tiles = static_cast<int>(tiles);
+  p.by_group = FastDiv(p.group);
+  p.by_tiles = FastDiv(p.tiles);
   p.grid = static_cast<int>(std::min(units, static_cast<double>(h->sm_count)));
-  if (few) CU(launch_kv8_attend_rows(h->tm_k, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
-  else CU(launch_kv8_attend_tc(h->tm_kp, h->tm_v, p, static_cast<cudaStream_t>(cuda_stream)));
+  if (few) CU(launch_kv8_attend_rows(p, static_cast<cudaStream_t>(cuda_stream)));
+  else CU(launch_kv8_attend_tc(p, static_cast<cudaStream_t>(cuda_stream)));
   return VLA_OK;
 }
 

@@ -5,22 +5,26 @@
 // The query rows of one K/V head are its tokens times its group of heads; a tile has 8 or 16.
 //
 // Few rows leave the cache bytes as the bound, so the work is split over the tokens alone,
-// equally over the CTAs (kv8.cuh). One thread feeds a ring of 32 KB stages with TMA; eight
-// warps each take 32 tokens of a stage at a time with a softmax of their own (reference
-// maximum, sum and outputs in registers), and the eight partial results meet in shared memory
-// once per item. An item that lies in one CTA is finished there; parts of an item go to a
-// workspace that a second kernel merges.
+// equally over the CTAs (kv8.cuh). A CTA's warps take the blocks of 64 tokens in turn, each
+// warp on its own: it copies a K block in as soon as the scores of the block that stood there
+// are done and a V block after the output, with a softmax of its own (reference maximum, sum
+// and outputs in registers). The warps' partial results meet in shared
+// memory once per item. An item that lies in one CTA is finished there; parts of an item go to
+// a workspace that a second kernel merges.
 //
-// The products run on E4M3 as the cache holds it, without widening: m16n8k32 on E4M3 takes
-// 3.8e3 multiply-adds a clock and SM here, m16n8k16 on fp16 1.0e3 plus two conversions for
-// four values. What is not E4M3 goes in as two terms:
-//   Q: each row times the power of two that brings its largest magnitude to [128, 256), then
-//      hi = e4m3(q), lo = e4m3(16 (q - hi)), summed apart, s = S_hi + S_lo / 16: exact for
-//      every bf16 value above 2^-14 of the largest, to 2^-21 of the largest below.
-//   P: relative to the maximum of its own 32 tokens, p = 256 exp2(x - m), hi = e4m3(p),
-//      lo = e4m3(16 (p - hi)): off by at most 2^-8 of p or 2^-22 of the largest of the 32. The
-//      product of the 32 tokens is added to the output in fp32 times exp2(m - M) s_V.
-// With 8 rows the two terms are the two halves of one 16-row instruction.
+// The products are m16n8k16 on fp16, transposed, so that tokens and dims are the sixteen and the
+// query rows the eight of an instruction: S^T = K Q^T, O^T += V^T P^T. (m16n8k32 takes E4M3
+// operands, but on this architecture it is made of conversions of both operands and fp16
+// products: at head_dim 128 a block took 1390 instructions, with the conversions of K and V
+// written out 1070, transposed about 600.)
+//   K, V widen to fp16 exactly.
+//   Q: each row times the power of two that brings its largest magnitude to [128, 256): exact
+//      for every bf16 value above 2^-24 of the largest.
+//   P: relative to the maximum of its own 64 tokens, fp16(exp2(x - m)): off by at most 2^-11 of p
+//      or 2^-25. The product of the 64 tokens is added to the output in fp32 times
+//      exp2(m - M) s_V.
+#include <float.h>
+
 #include "kernels.h"
 #include "kv8.cuh"
 #include "ptx.cuh"
@@ -29,131 +33,144 @@ namespace vla {
 
 namespace {
 
-constexpr int kWarps = 8;                    // consumer warps; warp 8 feeds the ring
-// Three warpgroups, the last one only for the ring's feeder. Registers: 168 a thread at
-// launch; the feeder's group goes down to 40 and the two others up to 232
-// (2 x 128 x 232 + 128 x 40 = 64512 = 384 x 168), which holds 16 x 256 outputs.
-constexpr int kThreads = 384;
-constexpr int kStageK = 16384;               // K bytes of a stage; V follows
-constexpr int kStage = 2 * kStageK;
-constexpr int kStages = 5;
 constexpr float kMoveBy = 32.0f;             // the reference maximum moves when passed by 2^32
 
 template <int D, int R>
-struct RowsSmem {
-  static constexpr int qfrag = D / 32 * 512 * (R / 8);            // A fragments of Q, 16 bytes a lane
-  static constexpr int q = kStages * kStage;
-  static constexpr int xch = q + qfrag;                           // [8 warps][R rows][columns] fp32
-  static constexpr int cols = D < 1024 / R ? D : 1024 / R;         // columns of a round of the exchange
-  static constexpr int ml = xch + kWarps * R * cols * 4;          // [8 warps][R rows] (maximum, sum)
-  static constexpr int misc = ml + kWarps * R * 8;                // row factors, scan
-  static constexpr int scale = misc + 64;                         // [stages][4 blocks] float4
-  static constexpr int bar = scale + kStages * 4 * 16;
-  static constexpr int total = bar + kStages * 16;
+struct RowsCfg {
+  // Warps of a CTA, each with `slots` K and V blocks in shared memory (up to 192 KB): enough to
+  // cover the latency of memory, and few enough warps that their products do not get in each
+  // other's way (12 warps with a slot each: 5 % slower than 6 with two at head_dim 128).
+  static constexpr int slots = D == 64 && R == 8 ? 3 : 2;
+  static constexpr int warps = D == 256 ? 3 : D == 128 ? 6 : 8;
+  static constexpr int block = D * 64;                            // bytes of a K or V block
+  static constexpr int qfrag = D / 16 * 32 * R;                   // B fragments of Q: 8 bytes a lane, step and 8 rows
+  static constexpr int cols = D < 64 ? D : 64;                    // columns of a round of the exchange
+  static constexpr int q = warps * slots * 2 * block;
+  static constexpr int xch = q + qfrag;                           // [warps][R rows][pitch] fp32
+  static constexpr int pitch = cols + 4;                          // floats: 4 row pairs x 8 dims touch all banks
+  static constexpr int ml = xch + warps * R * pitch * 4;          // [warps][R rows] (maximum, sum)
+  static constexpr int rowf = ml + warps * R * 8;                 // row factors
+  static constexpr int bar = rowf + 64;                           // [warps][slots] K, V
+  static constexpr int total = bar + warps * slots * 16;
 };
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint2& b) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+// The first of a sum.
+__device__ __forceinline__ void mma_f16_0(float (&c)[4], const uint32_t (&a)[4], const uint2& b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.0f));
+}
+// An 8 x 8 matrix of halves, row g in the four lanes 4 g + t, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// Four E4M3 bytes to two pairs of halves.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
-}
-
-// x, y as hi + lo E4M3 pairs, lo from `up` times the rest.
-__device__ __forceinline__ void split2(float x, float y, float up, uint32_t& hi, uint32_t& lo) {
-  const uint16_t h = f2_to_e4m3x2(x, y);
-  const uint32_t h2 = e4m3x2_to_h2(h);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  hi = h;
-  lo = f2_to_e4m3x2((x - f.x) * up, (y - f.y) * up);
 }
 
 }  // namespace
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 1)
-    kv8_attend_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                           const Kv8AttendParams p) {
-  using S = RowsSmem<D, R>;
-  constexpr int kPer = 256 / D;                 // blocks of a stage
-  constexpr int kSlices = 2 * kPer;             // 32-token slices of a stage
-  constexpr int kRows = R / 8;                  // rows a lane holds: gq, and gq + 8 if R is 16
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+__global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_kernel(const Kv8AttendParams p) {
+  using S = RowsCfg<D, R>;
+  constexpr int kWarps = S::warps;
+  constexpr int kN = R / 8;                     // eights of query rows
+  extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sm = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* rowf = reinterpret_cast<float*>(smem + S::misc);         // [R] score factors
-  const uint32_t full0 = sm + S::bar, empty0 = full0 + 8 * kStages;
+  float* rowf = reinterpret_cast<float*>(smem + S::rowf);         // [R] score factors
+  // slot s of this warp: its barriers for K and V, and its blocks
+  auto kfull = [&](int s) { return sm + S::bar + (warp * S::slots + s) * 16; };
+  auto kslot = [&](int s) { return sm + (warp * S::slots + s) * 2 * S::block; };
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, kWarps);
+  if (lane == 0) {
+    for (int s = 0; s < S::slots; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(kfull(s) + 8, 1);
     }
     fence_mbar_init();
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-    pdl_trigger();
   }
+  if (threadIdx.x == 0) pdl_trigger();
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
       if (kv8_tile(p, b, 0).slot < 0) report(p.err, kKv8BadRow);
+  __syncwarp();
   Kv8Walk w = kv8_walk(p);
-  __syncthreads();
-
   Kv8Segment g;
-  int it = 0;                                   // stages so far
-  bool ok = true;
-  if (warp >= kWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == kWarps && lane == 0) {
-      const uint64_t pol = policy_evict_first();
-      while (ok && kv8_next(p, w, g)) {
-        const size_t item = ((static_cast<size_t>(p.layer) * p.c.n_slots + g.row.slot) * p.c.n_kv + g.head) * p.c.nblk;
-        for (int j = 0; j < g.n; j += kPer, ++it) {
-          const int s = it % kStages, n = min(kPer, g.n - j);
-          if (it >= kStages && !mbar_wait(empty0 + 8 * s, (it / kStages - 1) & 1, p.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = full0 + 8 * s;
-          mbar_arrive_expect_tx(full, n * (2 * D * 64 + 16));
-          const size_t blk = item + g.blk + j;
-          bulk_load_g2s(sm + S::scale + s * 64, p.c.scale + blk, n * 16, full);
-          for (int i = 0; i < n; ++i) {
-            tma_load_2d(sm + s * kStage + i * D * 64, &tm_k, full, 0, static_cast<int>((blk + i) * D), pol);
-            tma_load_2d(sm + s * kStage + kStageK + i * D * 64, &tm_v, full, 0, static_cast<int>((blk + i) * D), pol);
-          }
-        }
-      }
-      // no copies left in flight: the last load of every stage has landed
-      const int from = it > kStages ? it - kStages : 0;
-      for (int i = from; i < it; ++i) mbar_wait(full0 + 8 * (i % kStages), (i / kStages) & 1, p.err);
-    }
-    return;
-  }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+  bool more = kv8_next(p, w, g);
 
-  const int gq = lane >> 2, t = lane & 3;       // fragment row (and column of B), and quad lane
-  const int swz = (gq >> 1) & 3;                // 64-byte swizzle of the rows this lane reads
-  while (kv8_next(p, w, g)) {
-    // ---- Q rows to E4M3 pairs, laid out as A fragments
+  // This warp's blocks: block `warp`, `warp` + kWarps, ... of each segment. The walk of the loads
+  // runs ahead by the number of slots, over the segments' ends.
+  auto item_of = [&](const Kv8Segment& x) {
+    return ((static_cast<size_t>(p.layer) * p.c.n_slots + x.row.slot) * p.c.n_kv + x.head) * p.c.nblk + x.blk;
+  };
+  Kv8Walk wl = w;
+  Kv8Segment gl = g;
+  bool morel = more;
+  int jl = warp;
+  auto skip = [&]() {                           // to the segment of the next block to load
+    while (morel && jl >= gl.n) {
+      morel = kv8_next(p, wl, gl);
+      jl = warp;
+    }
+  };
+  auto load = [&](uint32_t slot, const uint8_t* from, uint32_t full) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(full, S::block);
+      bulk_load_g2s(slot, from + (item_of(gl) + jl) * S::block, S::block, full);
+    }
+  };
+  skip();
+  for (int s = 0; s < S::slots && morel; ++s) {
+    load(kslot(s), p.c.k, kfull(s));
+    load(kslot(s) + S::block, p.c.v, kfull(s) + 8);
+    jl += kWarps;
+    skip();
+  }
+
+  // gq: row (token or dim) of an A fragment, query row of a B fragment; accumulators: rows gq and
+  // gq + 8, query rows 2 t and 2 t + 1
+  const int gq = lane >> 2, t = lane & 3;
+  const uint32_t lane_at = gq * 64 + ((t ^ ((gq >> 1) & 3)) << 4);   // chunk t of row gq, swizzled
+  int cur = 0;                                  // slot of the next block
+  uint32_t phase = 0;
+  bool ok = true;
+  for (; more; more = kv8_next(p, w, g)) {
+    // ---- Q rows to fp16, laid out as B fragments: word m of a lane's 16 dims of a panel (dims
+    // 64 p + 16 t + 4 m ..) is step 4 p + m
     const int rows = min(R, g.row.cnt * p.group - g.tile * R);
-    named_bar_sync(1, kWarps * 32);             // the last segment's readers of Q are done
+    __syncthreads();                            // the last segment's readers of Q are done
     for (int r = warp; r < R; r += kWarps) {
       constexpr int kPl = D / 32;               // values a lane
       float x[kPl];
       float am = 0.0f;
       const int row = g.tile * R + r;
-      const __nv_bfloat16* q = p.q + g.b * p.q_st[0] + (row / p.group) * p.q_st[1] +
-                               (g.head * p.group + row % p.group) * p.q_st[2];
+      const __nv_bfloat16* q = p.q + g.b * p.q_st[0] + p.by_group.div(row) * p.q_st[1] +
+                               (g.head * p.group + p.by_group.mod(row)) * p.q_st[2];
 #pragma unroll
       for (int i = 0; i < kPl; i += 2) {
         uint32_t v = 0;
@@ -170,351 +187,346 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = exp2i(-e);
 #pragma unroll
       for (int i = 0; i < kPl; i += 2) {
-        const int d = i * 32 + lane * 2;        // kk: 32 dims; c: 16-byte chunk; quad lane, byte
-        const int kk = d >> 5, c = (d >> 4) & 1, tq = (d >> 2) & 3, j = d & 3;
-        uint32_t hi, lo;
-        // an infinity has no E4M3 value: NaN, like the score it gives
-        float u = x[i] * inv, v = x[i + 1] * inv;
-        u = fmaf(u, 0.0f, u);
-        v = fmaf(v, 0.0f, v);
-        split2(u, v, 16.0f, hi, lo);
-        const int at = ((r & 7) * 4 + tq) * 16 + c * 8 + j;
-        if (R == 8) {
-          uint8_t* a = smem + S::q + kk * 512 + at;
-          *reinterpret_cast<uint16_t*>(a) = static_cast<uint16_t>(hi);
-          *reinterpret_cast<uint16_t*>(a + 4) = static_cast<uint16_t>(lo);
-        } else {
-          uint8_t* a = smem + S::q + kk * 1024 + at + (r >> 3) * 4;
-          *reinterpret_cast<uint16_t*>(a) = static_cast<uint16_t>(hi);
-          *reinterpret_cast<uint16_t*>(a + 512) = static_cast<uint16_t>(lo);
-        }
+        const int d = i * 32 + lane * 2;
+        const int m = (d >> 2) & 3, kk = 4 * (d >> 6) + m, tq = (d >> 4) & 3;
+        *reinterpret_cast<uint32_t*>(smem + S::q + ((kk * kN + (r >> 3)) * 32 + (r & 7) * 4 + tq) * 8 + (d & 2) * 2) =
+            pack_h2(x[i] * inv, x[i + 1] * inv);
       }
       if (lane == 0) rowf[r] = exp2i(e) * p.scale_log2;
     }
-    named_bar_sync(1, kWarps * 32);
+    __syncthreads();
 
     // ---- the visible ranges of this lane's rows, and of the tile
     const int r0 = g.tile * R, last = r0 + max(rows, 1) - 1;
-    int lo[kRows], hi[kRows], lo_first, hi_first, lo_last, hi_last;
-    float f[kRows], m[kRows], l[kRows];
+    int lo[kN][2], hi[kN][2], lo_first, hi_first, lo_last, hi_last;
+    float f[kN][2], m[kN][2], l[kN][2];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      kv8_seen(p, g.row, (r0 + gq + 8 * r) / p.group, lo[r], hi[r]);
-      f[r] = rowf[gq + 8 * r];
-      m[r] = -INFINITY;
-      l[r] = 0.0f;
-    }
-    kv8_seen(p, g.row, r0 / p.group, lo_first, hi_first);
-    kv8_seen(p, g.row, last / p.group, lo_last, hi_last);
-    uint4 qf[R == 8 ? D / 32 : 1];              // 8 rows: the fragments stay in registers
-    const uint4* qs = reinterpret_cast<const uint4*>(smem + S::q) + lane;
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * n + 2 * t + c;
+        kv8_seen(p, g.row, p.by_group.div(r0 + r), lo[n][c], hi[n][c]);
+        f[n][c] = rowf[r];
+        m[n][c] = -INFINITY;
+        l[n][c] = 0.0f;
+      }
+    kv8_seen(p, g.row, p.by_group.div(r0), lo_first, hi_first);
+    kv8_seen(p, g.row, p.by_group.div(last), lo_last, hi_last);
+    // with 8 rows the fragments of Q stay in registers
+    const uint2* qs = reinterpret_cast<const uint2*>(smem + S::q) + lane;
+    uint2 qf[R == 8 ? D / 16 : 1];
     if (R == 8) {
 #pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk) qf[R == 8 ? kk : 0] = qs[kk * 32];
+      for (int kk = 0; kk < D / 16; ++kk) qf[R == 8 ? kk : 0] = qs[kk * 32];
     }
+    const float4* scales = p.c.scale + item_of(g);
+    float4 next_sc = warp < g.n ? __ldg(scales + warp) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
-    float o[D / 8][2 * kRows];
+    float o[D / 16][kN][4];
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int c = 0; c < 2 * kRows; ++c) o[j][c] = 0.0f;
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[j][n][c] = 0.0f;
 
-    for (int j = 0; j < g.n; j += kPer, ++it) {
-      const int s = it % kStages;
-      const int base = (j / kPer) * kSlices;    // the segment's slices go round the warps
-      const int sl = (warp - base % kWarps + kWarps) % kWarps;
-      // every warp waits for every stage and releases it, also one it has no slice of: a warp
-      // that skipped a stage could take the slot's last phase for its next one
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(full0 + 8 * s, (it / kStages) & 1, p.err)) != 0;
-      const int bi = sl >> 1, wsl = sl & 1;
-      const int tok = (g.blk + j + bi) * kKv8Block + wsl * 32;
-      if (ok && sl < kSlices && j + bi < g.n && tok < hi_last && tok + 32 > lo_first) {
-        const uint32_t kb = sm + s * kStage + bi * D * 64 + (wsl * 32 + gq) * 64 + 4 * t;
-        const uint32_t vb = sm + s * kStage + kStageK + bi * D * 64 + gq * 64 + 4 * t;
-        const float4 sc = *reinterpret_cast<const float4*>(smem + S::scale + s * 64 + bi * 16);
-        // ---- scores: x[h][c] of token tok + 8 h + 2 t + (c & 1), row gq + 8 (c >> 1)
-        float x[4][2 * kRows];
-        {
-          float a[4][4] = {}, b[R == 8 ? 1 : 4][4] = {};
+    for (int j = warp; j < g.n; j += kWarps) {
+      const int tok = (g.blk + j) * kKv8Block;
+      const float4 sc = next_sc;
+      if (j + kWarps < g.n) next_sc = __ldg(scales + j + kWarps);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(kfull(cur), phase, p.err)) != 0;
+      const uint32_t kb = kslot(cur), vb = kb + S::block;
+      // ---- scores: x[h][n][c] of token tok + 16 h + gq + 8 (c >> 1), query row 8 n + 2 t + (c & 1)
+      float x[4][kN][4];
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            uint4 qa, qb;
-            if (R == 8) {
-              qa = qf[R == 8 ? kk : 0];
-            } else {
-              qa = qs[kk * 64];
-              qb = qs[kk * 64 + 32];
-            }
-            const uint32_t k0 = (kk >> 1) * 4096 + (((2 * (kk & 1)) ^ swz) << 4);
-            const uint32_t k1 = (kk >> 1) * 4096 + (((2 * (kk & 1) + 1) ^ swz) << 4);
+      for (int pp = 0; pp < D / 64; ++pp)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint32_t b0 = lds32(kb + k0 + h * 512), b1 = lds32(kb + k1 + h * 512);
-              mma_e4m3(a[h], qa, b0, b1);
-              if (R != 8) mma_e4m3(b[R == 8 ? 0 : h], qb, b0, b1);
+        for (int h = 0; h < 4; ++h) {
+          const uint4 k0 = lds128(kb + pp * 4096 + h * 1024 + lane_at);
+          const uint4 k1 = lds128(kb + pp * 4096 + h * 1024 + 512 + lane_at);
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a[4];
+            widen4(w0[i], a[0], a[2]);
+            widen4(w1[i], a[1], a[3]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+              const uint2 b = R == 8 ? qf[R == 8 ? 4 * pp + i : 0] : qs[((4 * pp + i) * kN + n) * 32];
+              if (pp == 0 && i == 0) mma_f16_0(x[h][n], a, b);
+              else mma_f16(x[h][n], a, b);
             }
           }
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int c = 0; c < 2 * kRows; ++c)
-              x[h][c] = R == 8 ? fmaf(a[h][c + 2], 0.0625f, a[h][c])
-                               : fmaf(b[R == 8 ? 0 : h][c], 0.0625f, a[h][c]);
         }
-        if (tok < lo_last || tok + 32 > hi_first) {      // some row does not see all of the slice
+      __syncwarp();                             // the K slot is free: the next block's K
+      if (morel) load(kb, p.c.k, kfull(cur));
+      if (tok < lo_last || tok + kKv8Block > hi_first) {   // some row does not see all of the block
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int c = 0; c < 2 * kRows; ++c) {
-              const int k = tok + 8 * h + 2 * t + (c & 1), r = c >> 1;
-              if (k < lo[r] || k >= hi[r]) x[h][c] = -INFINITY;
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int k = tok + 16 * h + gq + 8 * (c >> 1);
+              if (k < lo[n][c & 1] || k >= hi[n][c & 1]) x[h][n][c] = -INFINITY;
             }
-        }
-        // ---- weights relative to the slice's own maximum
-        float fac[kRows];
-        uint4 ph, pl;
+      }
+      // ---- weights relative to the block's own maximum
+      float fac[kN][2];
+      uint2 pb[4][kN];                          // B fragments of the four 16-token groups
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+      for (int n = 0; n < kN; ++n) {
+        float off[2], gk[2], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) mx = fmaxf(mx, fmaxf(x[h][2 * r], x[h][2 * r + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float gk = f[r] * sc.x, ms = mx * gk;
-          const bool move = ms > m[r] + kMoveBy || (m[r] == -INFINITY && ms > m[r]);
-          if (__any_sync(0xffffffffu, move)) {
-            const float nm = move ? ms : m[r];
-            const float k = nm == m[r] ? 1.0f : exp2_approx(m[r] - nm);
-            m[r] = nm;
-            l[r] *= k;
+          for (int h = 0; h < 4; ++h) mx = fmaxf(mx, fmaxf(x[h][n][c], x[h][n][c + 2]));
 #pragma unroll
-            for (int jj = 0; jj < D / 8; ++jj) {
-              o[jj][2 * r] *= k;
-              o[jj][2 * r + 1] *= k;
+          for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+          gk[c] = fmaxf(f[n][c] * sc.x, FLT_MIN);           // (0 would turn a masked score into NaN)
+          const float ms = mx * gk[c];
+          const bool move = ms > m[n][c] + kMoveBy || (m[n][c] == -INFINITY && ms > m[n][c]);
+          if (__any_sync(0xffffffffu, move)) {
+            const float nm = move ? ms : m[n][c];
+            const float k = nm == m[n][c] ? 1.0f : exp2_approx(m[n][c] - nm);
+            m[n][c] = nm;
+            l[n][c] *= k;
+#pragma unroll
+            for (int jj = 0; jj < D / 16; ++jj) {
+              o[jj][n][c] *= k;
+              o[jj][n][c + 2] *= k;
             }
           }
-          const float off = ms == -INFINITY ? 0.0f : 8.0f - ms;
-          float sum = 0.0f;
-          uint32_t wh[4], wl[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float u = exp2_approx(fmaf(x[h][2 * r], gk, off)), v = exp2_approx(fmaf(x[h][2 * r + 1], gk, off));
-            sum += u + v;
-            split2(u, v, 16.0f, wh[h], wl[h]);
-          }
-          const float k = ms == -INFINITY ? 0.0f : exp2_approx(ms - m[r] - 8.0f);
-          l[r] = fmaf(sum, k, l[r]);
-          fac[r] = k * sc.y;
-          const uint32_t h0 = wh[0] | (wh[1] << 16), h1 = wh[2] | (wh[3] << 16);
-          const uint32_t l0 = wl[0] | (wl[1] << 16), l1 = wl[2] | (wl[3] << 16);
-          if (R == 8) {
-            ph = make_uint4(h0, l0, h1, l1);
-          } else if (r == 0) {
-            ph.x = h0;
-            ph.z = h1;
-            pl.x = l0;
-            pl.z = l1;
-          } else {
-            ph.y = h0;
-            ph.w = h1;
-            pl.y = l0;
-            pl.w = l1;
-          }
+          off[c] = ms == -INFINITY ? 0.0f : -ms;
+          fac[n][c] = ms == -INFINITY ? 0.0f : exp2_approx(ms - m[n][c]);
         }
-        // ---- o += fac * P V
-        const uint32_t v0 = vb + (((2 * wsl) ^ swz) << 4), v1 = vb + (((2 * wsl + 1) ^ swz) << 4);
 #pragma unroll
-        for (int jj = 0; jj < D / 8; ++jj) {
-          const uint32_t b0 = lds32(v0 + jj * 512), b1 = lds32(v1 + jj * 512);
-          float y[4] = {};
-          if (R != 8) {
-            mma_e4m3(y, pl, b0, b1);
+        for (int h = 0; h < 4; ++h) {
+          float w[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] *= 0.0625f;
+          for (int c = 0; c < 4; ++c) {
+            w[c] = exp2_approx(fmaf(x[h][n][c], gk[c & 1], off[c & 1]));
+            sum[c & 1] += w[c];
           }
-          mma_e4m3(y, ph, b0, b1);
-          if (R == 8) {
-            o[jj][0] = fmaf(fmaf(y[2], 0.0625f, y[0]), fac[0], o[jj][0]);
-            o[jj][1] = fmaf(fmaf(y[3], 0.0625f, y[1]), fac[0], o[jj][1]);
-          } else {
+          pb[h][n] = make_uint2(transpose8(pack_h2(w[0], w[1])), transpose8(pack_h2(w[2], w[3])));
+        }
 #pragma unroll
-            for (int c = 0; c < 2 * kRows; ++c) o[jj][c] = fmaf(y[c], fac[c >> 1], o[jj][c]);
-          }
+        for (int c = 0; c < 2; ++c) {
+          l[n][c] = fmaf(sum[c], fac[n][c], l[n][c]);
+          fac[n][c] *= sc.y;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * s);
+      // ---- o += fac * P V
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(kfull(cur) + 8, phase, p.err)) != 0;
+#pragma unroll
+      for (int jj = 0; jj < D / 16; ++jj) {
+        const uint4 v0 = lds128(vb + jj * 1024 + lane_at), v1 = lds128(vb + jj * 1024 + 512 + lane_at);
+        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+        float y[kN][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a[4];
+          widen4(w0[i], a[0], a[2]);
+          widen4(w1[i], a[1], a[3]);
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            if (i == 0) mma_f16_0(y[n], a, pb[i][n]);
+            else mma_f16(y[n], a, pb[i][n]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[jj][n][c] = fmaf(y[n][c], fac[n][c & 1], o[jj][n][c]);
+      }
+      __syncwarp();                             // the V slot is free: the next block's V
+      if (morel) {
+        load(vb, p.c.v, kfull(cur) + 8);
+        jl += kWarps;
+        skip();
+      }
+      if (++cur == S::slots) {
+        cur = 0;
+        phase ^= 1;
+      }
     }
 
-    // ---- the eight warps' results
+    // ---- the warps' results
     float2* ml = reinterpret_cast<float2*>(smem + S::ml);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t == 0) ml[warp * R + gq + 8 * r] = make_float2(m[r], l[r]);
-    }
-    named_bar_sync(1, kWarps * 32);
-    float fac[kRows];
+    for (int n = 0; n < kN; ++n)
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      float mm = -INFINITY;
-      for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * R + gq + 8 * r].x);
-      fac[r] = m[r] == -INFINITY ? 1.0f : exp2_approx(m[r] - mm);
-    }
-    // this thread's output: row rr, kCols columns of each round of S::cols
-    constexpr int kCols = R * S::cols / (kWarps * 32);
-    const int rr = threadIdx.x / (S::cols / kCols), cc = (threadIdx.x % (S::cols / kCols)) * kCols;
-    float mm = -INFINITY, ll = 0.0f;
-    for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * R + rr].x);
-    for (int i = 0; i < kWarps; ++i) {
-      const float2 v = ml[i * R + rr];
-      ll += v.y * (v.x == -INFINITY ? 1.0f : exp2_approx(v.x - mm));
-    }
-    const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
-    const int row = r0 + rr;
-    const int qi = row / p.group, qh = g.head * p.group + row % p.group;
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], i);
+        if (gq == 0) ml[warp * R + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
+      }
+    __syncthreads();
+    float fac[kN][2];
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mm = -INFINITY;
+        for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * R + 8 * n + 2 * t + c].x);
+        fac[n][c] = m[n][c] == -INFINITY ? 1.0f : exp2_approx(m[n][c] - mm);
+      }
     const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
-    float* ws = p.ws + (static_cast<size_t>(slot) * R + rr) * D;
-    __nv_bfloat16* dst = p.out + g.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
     float* xb = reinterpret_cast<float*>(smem + S::xch);
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += S::cols) {
 #pragma unroll
-      for (int jj = 0; jj < S::cols / 8; ++jj)
+      for (int jj = 0; jj < S::cols / 16; ++jj)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          *reinterpret_cast<float2*>(xb + (warp * R + gq + 8 * r) * S::cols + jj * 8 + 2 * t) =
-              make_float2(o[c0 / 8 + jj][2 * r] * fac[r], o[c0 / 8 + jj][2 * r + 1] * fac[r]);
-      named_bar_sync(1, kWarps * 32);
-      if (rr < rows) {
-        float v[kCols] = {};
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) v[c] += xb[(i * R + rr) * S::cols + cc + c];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const int d = c0 + cc + c;
-          if (!g.whole) ws[d] = v[c];
-          else if (d < p.c.D) dst[d] = __float2bfloat16_rn(v[c] * norm);
+          for (int c = 0; c < 4; ++c)
+            xb[(warp * R + 8 * n + 2 * t + (c & 1)) * S::pitch + jj * 16 + gq + 8 * (c >> 1)] =
+                o[c0 / 16 + jj][n][c] * fac[n][c & 1];
+      __syncthreads();
+      for (int i = threadIdx.x; i < rows * (S::cols / 2); i += kWarps * 32) {
+        const int rr = i / (S::cols / 2), cc = (i % (S::cols / 2)) * 2, d = c0 + cc;
+        float mm = -INFINITY, ll = 0.0f;
+        for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, ml[k * R + rr].x);
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 y = *reinterpret_cast<const float2*>(xb + (k * R + rr) * S::pitch + cc);
+          const float2 z = ml[k * R + rr];
+          v.x += y.x;
+          v.y += y.y;
+          ll += z.y * (z.x == -INFINITY ? 1.0f : exp2_approx(z.x - mm));
+        }
+        const int row = r0 + rr, qi = p.by_group.div(row), qh = g.head * p.group + row - qi * p.group;
+        if (!g.whole) {
+          *reinterpret_cast<float2*>(p.ws + (static_cast<size_t>(slot) * R + rr) * D + d) = v;
+          if (d == 0) p.ws_ml[slot * R + rr] = make_float2(mm, ll);
+        } else if (d < p.c.D) {
+          const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
+          *reinterpret_cast<__nv_bfloat162*>(p.out + g.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2] + d) =
+              __floats2bfloat162_rn(v.x * norm, v.y * norm);
+          if (d == 0 && p.lse)
+            p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] =
+                ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
         }
       }
-      named_bar_sync(1, kWarps * 32);
-    }
-    if (cc == 0 && rr < rows) {
-      if (!g.whole)
-        p.ws_ml[slot * R + rr] = make_float2(mm, ll);
-      else if (p.lse)
-        p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] =
-            ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+      __syncthreads();
     }
   }
 }
 
-// Merges the parts of the items that more than one CTA worked on. CTA (x, y) looks at the cut
-// before part y + 1: if it is the first cut inside an item, it merges kMergeWarps / W rows of
-// that item, W warps a row (W = 1 for the many rows of few parts, all for few rows of many
-// parts): each warp sums every W-th part, a lane D / 32 columns, and the W sums are joined in
-// order in shared memory.
+// ---- merging the parts of the items that more than one CTA worked on
+
+// The item that the cut before part `cut` lies in, if it is the first cut inside that item.
+struct Kv8Cut {
+  int b, tile, head, rows;      // rows: query rows of the tile
+  int u0, c0, c1;               // the item's first unit; parts c0 .. c1 - 1 meet it
+};
+__device__ __forceinline__ bool kv8_cut(const Kv8AttendParams& p, const Kv8Line& line, int cut, Kv8Cut& r) {
+  const int uc = kv8_begin(line, cut);
+  if (uc >= line.total) return false;
+  int inside;
+  const int e = kv8_find(p, line, uc, &inside);
+  const Kv8Tile row = kv8_tile(p, p.by_tiles.div(e), p.by_tiles.mod(e));
+  r.u0 = uc - inside % row.units;
+  if (uc == r.u0 || kv8_begin(line, cut - 1) > r.u0) return false;
+  const int u1 = r.u0 + row.units;
+  r.b = p.by_tiles.div(e);
+  r.tile = e - r.b * p.tiles;
+  r.head = inside / row.units;
+  r.rows = min(p.tile_rows, row.cnt * p.group - r.tile * p.tile_rows);
+  r.c0 = cut - 1;
+  // (parts that meet the item have units: the cuts inside an item differ)
+  r.c1 = min(p.grid, cut + (line.per > 0 ? (u1 - uc - 1) / line.per + 1 : u1 - uc));
+  while (r.c1 > cut && kv8_begin(line, r.c1 - 1) >= u1) --r.c1;
+  return true;
+}
+// Place of a part in the workspace: the item in which a CTA's range starts is its first, one
+// that starts later its second.
+__device__ __forceinline__ int kv8_slot(const Kv8Line& line, const Kv8Cut& r, int c) {
+  return 2 * c + (kv8_begin(line, c) >= r.u0 ? 0 : 1);
+}
+
 constexpr int kMergeWarps = 8;
-template <int D, int W>
-__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Kv8AttendParams p) {
+
+// Few rows, as a rule of many parts: a CTA per (row, cut). Each warp sums every eighth part, a
+// lane D / 32 columns; the eight sums are joined in order in shared memory.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_rows_kernel(const Kv8AttendParams p) {
+  constexpr int W = kMergeWarps;
   constexpr int kPl = D / 32 >= 4 ? D / 32 : 4;          // columns a lane, in groups of 4
   constexpr int kLanes = D / kPl;
   constexpr int kG = kPl / 4;
-  __shared__ float2 sml[kMergeWarps];
-  __shared__ float4 so[W > 1 ? kMergeWarps : 1][kG][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float2 sml[W];
+  __shared__ float4 so[W][kG][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x;
   const Kv8Line line = kv8_line(p);
-  const int cut = blockIdx.y + 1, uc = kv8_begin(line, cut);
-  int inside = 0, e = 0, u0 = uc, u1 = uc;
-  Kv8Tile row{};
-  if (uc < line.total) {
-    e = kv8_find(p, line, uc, &inside);
-    row = kv8_tile(p, e / p.tiles, e % p.tiles);
-    u0 = uc - inside % row.units;
-    u1 = u0 + row.units;
-  }
+  Kv8Cut cut;
+  const bool mine = kv8_cut(p, line, blockIdx.y + 1, cut);
   pdl_wait();
-  // the first cut inside the item (parts without units have their cuts at the same unit)
-  if (uc == u0 || kv8_begin(line, cut - 1) > u0) return;
-  const int b = e / p.tiles, tile = e % p.tiles, head = inside / row.units;
-  const int rows = min(p.tile_rows, row.cnt * p.group - tile * p.tile_rows);
-  const int r = blockIdx.x * (kMergeWarps / W) + warp / W, share = warp % W;
-  if (blockIdx.x * (kMergeWarps / W) >= rows) return;
-  // parts cut - 1 .. c1 - 1 meet the item; all have units, as the cuts inside an item differ
-  int c1 = min(p.grid, cut + (line.per > 0 ? (u1 - uc - 1) / line.per + 1 : u1 - uc));
-  while (c1 > cut && kv8_begin(line, c1 - 1) >= u1) --c1;
+  if (!mine || r >= cut.rows) return;
   float mm = -INFINITY, ll = 0.0f;
   float4 v[kG] = {};
-  if (r < rows) {
-    for (int c0 = cut - 1 + share; c0 < c1; c0 += 32 * W) {
-      // 32 parts' maxima and sums at once, a lane each
-      const int c = c0 + lane * W;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      int at = 0;
-      if (c < c1) {
-        // the item in which a CTA's range starts is its first; one that starts later, its second
-        at = (2 * c + (kv8_begin(line, c) >= u0 ? 0 : 1)) * p.tile_rows + r;
-        ml = p.ws_ml[at];
-      }
-      float nm = ml.x;
+  for (int c0 = cut.c0 + warp; c0 < cut.c1; c0 += 32 * W) {
+    // 32 parts' maxima and sums at once, a lane each
+    const int c = c0 + lane * W;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    int at = 0;
+    if (c < cut.c1) {
+      at = kv8_slot(line, cut, c) * p.tile_rows + r;
+      ml = p.ws_ml[at];
+    }
+    float nm = ml.x;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
-      nm = fmaxf(nm, mm);
-      const float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - nm);
-      mm = nm;
-      ll *= k;
+    for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
+    nm = fmaxf(nm, mm);
+    const float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - nm);
+    mm = nm;
+    ll *= k;
 #pragma unroll
-      for (int i = 0; i < kG; ++i) v[i] = make_float4(v[i].x * k, v[i].y * k, v[i].z * k, v[i].w * k);
-      const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - mm);
-      const int n = min(32, (c1 - c0 + W - 1) / W);
+    for (int i = 0; i < kG; ++i) v[i] = make_float4(v[i].x * k, v[i].y * k, v[i].z * k, v[i].w * k);
+    const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - mm);
+    const int n = min(32, (cut.c1 - c0 + W - 1) / W);
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const int ai = __shfl_sync(0xffffffffu, at, i);
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        ll = fmaf(__shfl_sync(0xffffffffu, ml.y, i), fi, ll);
-        if (lane < kLanes) {
-          const float4* x = reinterpret_cast<const float4*>(p.ws + static_cast<size_t>(ai) * D) + lane;
+    for (int i = 0; i < n; ++i) {
+      const int ai = __shfl_sync(0xffffffffu, at, i);
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      ll = fmaf(__shfl_sync(0xffffffffu, ml.y, i), fi, ll);
+      if (lane < kLanes) {
+        const float4* x = reinterpret_cast<const float4*>(p.ws + static_cast<size_t>(ai) * D) + lane;
 #pragma unroll
-          for (int j = 0; j < kG; ++j) {
-            const float4 y = x[j * kLanes];
-            v[j] = make_float4(fmaf(y.x, fi, v[j].x), fmaf(y.y, fi, v[j].y), fmaf(y.z, fi, v[j].z), fmaf(y.w, fi, v[j].w));
-          }
+        for (int j = 0; j < kG; ++j) {
+          const float4 y = x[j * kLanes];
+          v[j] = make_float4(fmaf(y.x, fi, v[j].x), fmaf(y.y, fi, v[j].y), fmaf(y.z, fi, v[j].z), fmaf(y.w, fi, v[j].w));
         }
       }
     }
   }
-  if (W > 1) {
-    if (lane == 0) sml[warp] = make_float2(mm, ll);
+  if (lane == 0) sml[warp] = make_float2(mm, ll);
 #pragma unroll
-    for (int j = 0; j < kG; ++j) so[W > 1 ? warp : 0][j][lane] = v[j];
-    __syncthreads();
-    if (share != 0 || r >= rows) return;
-    float m0 = mm;
-    for (int i = 1; i < W; ++i) m0 = fmaxf(m0, sml[warp + i].x);
-    float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - m0);
-    ll *= k;
+  for (int j = 0; j < kG; ++j) so[warp][j][lane] = v[j];
+  __syncthreads();
+  if (warp != 0) return;
+  float m0 = mm;
+  for (int i = 1; i < W; ++i) m0 = fmaxf(m0, sml[i].x);
+  float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - m0);
+  ll *= k;
 #pragma unroll
-    for (int j = 0; j < kG; ++j) v[j] = make_float4(v[j].x * k, v[j].y * k, v[j].z * k, v[j].w * k);
-    for (int i = 1; i < W; ++i) {
-      const float2 y = sml[warp + i];
-      k = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - m0);
-      ll = fmaf(y.y, k, ll);
+  for (int j = 0; j < kG; ++j) v[j] = make_float4(v[j].x * k, v[j].y * k, v[j].z * k, v[j].w * k);
+  for (int i = 1; i < W; ++i) {
+    const float2 y = sml[i];
+    k = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - m0);
+    ll = fmaf(y.y, k, ll);
 #pragma unroll
-      for (int j = 0; j < kG; ++j) {
-        const float4 z = so[W > 1 ? warp + i : 0][j][lane];
-        v[j] = make_float4(fmaf(z.x, k, v[j].x), fmaf(z.y, k, v[j].y), fmaf(z.z, k, v[j].z), fmaf(z.w, k, v[j].w));
-      }
+    for (int j = 0; j < kG; ++j) {
+      const float4 z = so[i][j][lane];
+      v[j] = make_float4(fmaf(z.x, k, v[j].x), fmaf(z.y, k, v[j].y), fmaf(z.z, k, v[j].z), fmaf(z.w, k, v[j].w));
     }
-    mm = m0;
   }
-  if (r >= rows) return;
-  const int q = tile * p.tile_rows + r;
-  const int qi = q / p.group, qh = head * p.group + q % p.group;
+  const int q = cut.tile * p.tile_rows + r;
+  const int qi = p.by_group.div(q), qh = cut.head * p.group + p.by_group.mod(q);
   const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
-  __nv_bfloat16* dst = p.out + b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
+  __nv_bfloat16* dst = p.out + cut.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
   if (lane < kLanes)
 #pragma unroll
     for (int j = 0; j < kG; ++j) {
@@ -527,14 +539,65 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_kernel(const Kv8At
       }
     }
   if (lane == 0 && p.lse)
-    p.lse[(static_cast<size_t>(b) * p.n_q + qi) * p.n_heads + qh] =
+    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] =
+        ll == 0.0f ? -INFINITY : (m0 + log2f(ll)) * 0.6931471805599453f;
+}
+
+// Many rows: a CTA per (32 rows, cut); a lane is a row, a warp takes D / 8 of its columns. Parts
+// are laid out [D / 4][rows][4], so a warp's reads are in line.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_tiles_kernel(const Kv8AttendParams p) {
+  constexpr int kG = D / 4 / kMergeWarps;                // groups of four columns a thread
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x * 32 + lane;
+  const Kv8Line line = kv8_line(p);
+  Kv8Cut cut;
+  const bool mine = kv8_cut(p, line, blockIdx.y + 1, cut);
+  pdl_wait();
+  if (!mine || r >= cut.rows) return;
+  float mm = -INFINITY, ll = 0.0f;
+  for (int c = cut.c0; c < cut.c1; ++c) mm = fmaxf(mm, p.ws_ml[kv8_slot(line, cut, c) * p.tile_rows + r].x);
+  float4 v[kG] = {};
+  for (int c = cut.c0; c < cut.c1; ++c) {
+    const int slot = kv8_slot(line, cut, c);
+    const float2 ml = p.ws_ml[slot * p.tile_rows + r];
+    const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - mm);
+    ll = fmaf(ml.y, f, ll);
+    const float4* x = reinterpret_cast<const float4*>(p.ws + static_cast<size_t>(slot) * p.tile_rows * D) + r;
+#pragma unroll
+    for (int j = 0; j < kG; ++j) {
+      const float4 y = x[(warp * kG + j) * p.tile_rows];
+      v[j] = make_float4(fmaf(y.x, f, v[j].x), fmaf(y.y, f, v[j].y), fmaf(y.z, f, v[j].z), fmaf(y.w, f, v[j].w));
+    }
+  }
+  const int q = cut.tile * p.tile_rows + r;
+  const int qi = p.by_group.div(q), qh = cut.head * p.group + p.by_group.mod(q);
+  const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
+  __nv_bfloat16* dst = p.out + cut.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
+#pragma unroll
+  for (int j = 0; j < kG; j += 2) {
+    const int d = (warp * kG + j) * 4;
+    if (d < p.c.D) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[j + i].x * norm, v[j + i].y * norm);
+        const __nv_bfloat162 y = __floats2bfloat162_rn(v[j + i].z * norm, v[j + i].w * norm);
+        o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+        o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      *reinterpret_cast<uint4*>(dst + d) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (warp == 0 && p.lse)
+    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] =
         ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
-template <int D, int W>
-static cudaError_t launch_merge(const Kv8AttendParams& p, cudaStream_t s) {
+cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
+  if (p.grid < 2) return cudaSuccess;
+  const bool few = p.tile_rows <= 16;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.tile_rows + kMergeWarps / W - 1) / (kMergeWarps / W), p.grid - 1);
+  cfg.gridDim = dim3(few ? p.tile_rows : p.tile_rows / 32, p.grid - 1);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
@@ -542,42 +605,36 @@ static cudaError_t launch_merge(const Kv8AttendParams& p, cudaStream_t s) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<D, W>, p);
-}
-
-cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
-  if (p.grid < 2) return cudaSuccess;
-  const bool few = p.tile_rows <= 16;
-  if (p.c.Ds == 64) return few ? launch_merge<64, 8>(p, s) : launch_merge<64, 1>(p, s);
-  if (p.c.Ds == 128) return few ? launch_merge<128, 8>(p, s) : launch_merge<128, 1>(p, s);
-  return few ? launch_merge<256, 8>(p, s) : launch_merge<256, 1>(p, s);
+  switch (p.c.Ds) {
+    case 64: return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<64> : kv8_merge_tiles_kernel<64>, p);
+    case 128: return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<128> : kv8_merge_tiles_kernel<128>, p);
+    default: return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<256> : kv8_merge_tiles_kernel<256>, p);
+  }
 }
 
 template <int D, int R>
-static cudaError_t launch_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
-                               cudaStream_t s) {
+static cudaError_t launch_rows(const Kv8AttendParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = RowsSmem<D, R>::total + 1024;
+  cfg.blockDim = dim3(RowsCfg<D, R>::warps * 32);
+  cfg.dynamicSmemBytes = RowsCfg<D, R>::total;
   cfg.stream = s;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_attend_rows_kernel<D, R>, tm_k, tm_v, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_attend_rows_kernel<D, R>, p);
   return e != cudaSuccess ? e : launch_kv8_merge(p, s);
 }
 
-cudaError_t launch_kv8_attend_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
-                                   cudaStream_t s) {
+cudaError_t launch_kv8_attend_rows(const Kv8AttendParams& p, cudaStream_t s) {
   const bool r8 = p.tile_rows == 8;
-  if (p.c.Ds == 64) return r8 ? launch_rows<64, 8>(tm_k, tm_v, p, s) : launch_rows<64, 16>(tm_k, tm_v, p, s);
-  if (p.c.Ds == 128) return r8 ? launch_rows<128, 8>(tm_k, tm_v, p, s) : launch_rows<128, 16>(tm_k, tm_v, p, s);
-  return r8 ? launch_rows<256, 8>(tm_k, tm_v, p, s) : launch_rows<256, 16>(tm_k, tm_v, p, s);
+  if (p.c.Ds == 64) return r8 ? launch_rows<64, 8>(p, s) : launch_rows<64, 16>(p, s);
+  if (p.c.Ds == 128) return r8 ? launch_rows<128, 8>(p, s) : launch_rows<128, 16>(p, s);
+  return r8 ? launch_rows<256, 8>(p, s) : launch_rows<256, 16>(p, s);
 }
 
 template <int D, int R>
 static cudaError_t configure_rows() {
-  static_assert(RowsSmem<D, R>::total + 1024 <= 232448, "shared memory of a CTA");
+  static_assert(RowsCfg<D, R>::total <= 232448, "shared memory of a CTA");
   return cudaFuncSetAttribute(kv8_attend_rows_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              RowsSmem<D, R>::total + 1024);
+                              RowsCfg<D, R>::total);
 }
 
 cudaError_t configure_kv8_kernels() {

@@ -11,22 +11,27 @@
 //               [128, 256), hi = e4m3(q), lo = e4m3(q - hi). Exact for bf16 values above
 //               2^-10 of the largest, else to 2^-17 of it. Two E4M3 products take as long as
 //               one 16-bit product, and K needs no widening.
-//   P           fp16, exp2(s + log2 s_V - m + 7): the V scale enters through the exponent and
-//               leaves the sum in fp32; written over S in tensor memory, from where the
-//               second product takes it. 2^7 lifts the range: weights down to 2^-31 of the
-//               largest keep their place.
+//   P           fp16, exp2(s + log2 s_V - m + 2): the V scale enters through the exponent and
+//               leaves the sum in fp32; written over S in tensor memory, from where the second
+//               product takes it.
 //   O += P V    kind::f16. Four warps widen V blocks to fp16 (exact) in the 128-byte swizzled
 //               K-major layout; both query tiles use each widened block.
-// m moves only when a tile's maximum passes it by more than 2^8 (then O in tensor memory is
-// rescaled), so P stays below 2^15.
+// The row's reference m moves (and O in tensor memory is rescaled) only when a block's maximum
+// passes it by more than 2^13: fp16 then holds P from 2^15 down to steps of 2^-26 of the
+// reference, so that n keys behind a far larger one lose at most n 2^-27 of the sum.
 //
-// Two lanes of work keep the tensor pipe busy while the softmax of the other lane runs:
-//   head_dim <= 128, more than 128 rows: lane i is query tile i (128 rows), all keys.
-//   head_dim <= 128, up to 128 rows: lane i takes every second unit of keys for the same rows,
-//     with an output of its own; the two outputs are joined at the end.
-//   head_dim 256: one tile and one output (256 columns); lane i is one of two S buffers, the
-//     two softmax groups each take half of a unit's keys.
-// Warps: 0 TMA, 1 MMA, 4..7 and 8..11 softmax (one thread a row), 12..15 widening of V.
+// The tensor pipe and the softmax of a lane depend on each other, so there are two lanes with
+// two S buffers of 64 keys each: a buffer's next scores are issued when the output of its last
+// weights is done, and a softmax group always has its next scores waiting.
+//   head_dim <= 128, more than 128 rows: lane i is query tile i (128 rows), all blocks.
+//   head_dim <= 128, up to 128 rows: lane i takes every second block for the same rows, with an
+//     output of its own; the two outputs are joined at the end.
+//   head_dim 256: lane i takes every second block; one output (256 columns), for which the row's
+//     reference maximum goes from block to block between the two groups.
+// Warps: 0 loads of K, 2 loads of V, 1 scores, 3 outputs, 4..7 and 8..11 softmax of lane 0 and 1 (one thread
+// a row), 12..15 widening of V.
+#include <float.h>
+
 #include "kernels.h"
 #include "kv8.cuh"
 #include "ptx.cuh"
@@ -35,27 +40,26 @@ namespace vla {
 
 namespace {
 
-constexpr int kKeys = 128;                   // keys of a unit (two blocks)
 constexpr int kThreads = 512;
 // Registers: 128 a thread at launch; the softmax groups go up to 200, the two others down to
 // 56 (2 x 128 x 200 + 2 x 128 x 56 = 65536 = 512 x 128).
-constexpr float kLift = 7.0f;
+constexpr float kLag = 13.0f, kLift = 2.0f;   // see m below
 
 template <int D>
 struct Tc {
-  static constexpr bool two = D <= 128;                  // two query tiles a CTA
+  static constexpr bool two = D <= 128;                  // two query tiles, or two outputs
   static constexpr int rows = two ? 256 : 128;
-  static constexpr int nk = D == 256 ? 2 : 3;            // K stages of a unit
+  static constexpr int nk = D == 256 ? 4 : 6;            // K blocks
   static constexpr int nv = D == 256 ? 2 : 4;            // V blocks as stored, and widened
   static constexpr int q_half = 128 * D;                 // one term of one tile
   static constexpr int v16 = 0;                          // 128-byte swizzle: 1024-byte aligned
   static constexpr int q = v16 + nv * D * 128;           // [tile][term][D / 64 panels][128 rows][64]
   static constexpr int k = q + (two ? 2 : 1) * 2 * q_half;
-  static constexpr int v8 = k + nk * D * kKeys;
-  static constexpr int xch = v8 + nv * D * 64;           // [2][2][128] floats
+  static constexpr int v8 = k + nk * D * 64;
+  static constexpr int xch = v8 + nv * D * 64;           // [2][128] reference maxima; (maximum, sum) at the end
   static constexpr int bar = xch + 2048;
   static constexpr int total = bar + 512;
-  static constexpr int o_col = 256;                      // tensor memory: S 0 and 128, O from 256
+  static constexpr int o_col = 256;                      // tensor memory: S buffers 0, 64, 128, 192; O
 };
 
 // Operand descriptors in two words. Low: start address >> 4 and leading offset (unused, 1);
@@ -103,6 +107,23 @@ __device__ __forceinline__ void umma_commit_if(uint32_t lead, uint32_t bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(lead), "r"(bar)
       : "memory");
 }
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -135,32 +156,66 @@ __device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* 
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A segment's units and how the lanes share them.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {   // one 32-byte sector
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Bounded wait for a phase in few instructions: each try suspends the thread for up to a
+// millisecond, 2000 of them give up. (Five roles run on an SM at once, and short loops are what
+// its instruction caches need.)
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int* err) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+      "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, 2000;\n\t@p bra TRY;\n\tsetp.ne.u32 p, 0, 0;\n\t"
+      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__builtin_expect(!ok, 0)) report(err, kDevTimeout);
+  return ok != 0;
+}
+
+// How the lanes share a segment. Step k of lane i works in S buffer 2 i + (k & 1); scores and
+// outputs are issued in the order (lane 0, 0), (lane 1, 0), (lane 0, 1), ... (t = 2 k + lane).
 struct Plan {
-  int units;
-  bool tiles;            // lane = query tile (else: lane = every second unit, or S buffer)
+  bool tiles;            // lane = query tile, every block a step of both; else every second block
+  int steps[2];          // of each lane
 };
 template <int D>
 __device__ __forceinline__ Plan make_plan(const Kv8AttendParams& p, const Kv8Segment& g) {
   Plan r;
-  r.units = (g.n + 1) / 2;
   r.tiles = Tc<D>::two && g.row.cnt * p.group - g.tile * Tc<D>::rows > 128;
+  r.steps[0] = r.tiles ? g.n : (g.n + 1) / 2;
+  r.steps[1] = r.tiles ? g.n : g.n / 2;
   return r;
+}
+// Parities of the buffers' barriers: bit b of `ph` is that of buffer b's first use in a segment.
+__device__ __forceinline__ uint32_t buf_parity(uint32_t ph, int lane_of, int k) {
+  return ((ph >> (2 * lane_of + (k & 1))) ^ (k >> 1)) & 1;
+}
+__device__ __forceinline__ uint32_t next_phases(uint32_t ph, const Plan& pl) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    ph ^= (((pl.steps[i] + 1) >> 1) & 1) << (2 * i) | ((pl.steps[i] >> 1) & 1) << (2 * i + 1);
+  return ph;
 }
 
 }  // namespace
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv8_attend_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const Kv8AttendParams p) {
+    kv8_attend_tc_kernel(const Kv8AttendParams p) {
   using S = Tc<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sm = smem_u32(smem);
   const uint32_t kfull = sm + S::bar, kempty = kfull + 8 * S::nk;
   const uint32_t rfull = kempty + 8 * S::nk, rempty = rfull + 8 * S::nv;      // V as stored
   const uint32_t vfull = rempty + 8 * S::nv, vempty = vfull + 8 * S::nv;      // V widened
-  const uint32_t sfull = vempty + 8 * S::nv, pfull = sfull + 16, odone = pfull + 32, qfull = odone + 16;   // pfull: [lane][block]
+  const uint32_t sfull = vempty + 8 * S::nv, pfull = sfull + 32, odone = pfull + 32, qfull = odone + 32;   // [buffer]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::bar + 504);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -175,16 +230,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(vfull + 8 * i, 4);
       mbar_init(vempty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(sfull + 8 * i, 1);
-      mbar_init(pfull + 16 * i, 4);
-      mbar_init(pfull + 16 * i + 8, 4);
+      mbar_init(pfull + 8 * i, 4);
       mbar_init(odone + 8 * i, 1);
     }
     mbar_init(qfull, 8);
     fence_mbar_init();
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
     pdl_trigger();
   }
   if (warp == 1) {
@@ -204,137 +256,104 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0 && lane == 0) {
-      // ---- loads: a unit of K, its blocks of V, in the order they are used
-      const uint64_t pol = policy_evict_last();
-      int kt = 0, vt = 0;
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      // ---- loads: warp 0 the K blocks, warp 2 the V blocks
+      const uint8_t* src = warp == 0 ? p.c.k : p.c.v;
+      const uint32_t full = warp == 0 ? kfull : rfull, empty = warp == 0 ? kempty : rempty;
+      const uint32_t dst = sm + (warp == 0 ? S::k : S::v8);
+      const int ring = warp == 0 ? S::nk : S::nv;
+      int n = 0, s = 0;
+      uint32_t ph = 1;
       while (ok && kv8_next(p, w, g)) {
         const size_t blk0 =
             ((static_cast<size_t>(p.layer) * p.c.n_slots + g.row.slot) * p.c.n_kv + g.head) * p.c.nblk + g.blk;
-        for (int j = 0; j < g.n && ok; j += 2, ++kt) {
-          const int n = min(2, g.n - j), s = kt % S::nk;
-          if (kt >= S::nk && !mbar_wait(kempty + 8 * s, (kt / S::nk - 1) & 1, p.err)) {
+        for (int j = 0; j < g.n; ++j, ++n) {
+          if (n >= ring && !mbar_wait(empty + 8 * s, ph, p.err)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(kfull + 8 * s, n * D * 64);
-          for (int i = 0; i < n; ++i)
-            // block i of panel c stands behind block 0's: rows of one panel of 128 keys are in line
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_2d(sm + S::k + s * D * kKeys + (c * 128 + i * 64) * 64, &tm_k, kfull + 8 * s, 0,
-                          static_cast<int>((blk0 + j + i) * D + c * 64), pol);
-          for (int i = 0; i < n; ++i, ++vt) {
-            const int r = vt % S::nv;
-            if (vt >= S::nv && !mbar_wait(rempty + 8 * r, (vt / S::nv - 1) & 1, p.err)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(rfull + 8 * r, D * 64);
-            tma_load_2d(sm + S::v8 + r * D * 64, &tm_v, rfull + 8 * r, 0, static_cast<int>((blk0 + j + i) * D), pol);
+          mbar_arrive_expect_tx(full + 8 * s, D * 64);
+          bulk_load_g2s(dst + s * D * 64, src + (blk0 + j) * (D * 64), D * 64, full + 8 * s);
+          if (++s == ring) {
+            s = 0;
+            ph ^= 1;
           }
         }
       }
       // no copies left in flight
-      for (int i = kt > S::nk ? kt - S::nk : 0; i < kt; ++i) mbar_wait(kfull + 8 * (i % S::nk), (i / S::nk) & 1, p.err);
-      for (int i = vt > S::nv ? vt - S::nv : 0; i < vt; ++i) mbar_wait(rfull + 8 * (i % S::nv), (i / S::nv) & 1, p.err);
-    } else if (warp == 1) {
-      // ---- products, by the converged warp. All that can wait before P arrives is done before:
-      // once per unit the V blocks, the next unit's K and the operands' words
+      for (int i = n > ring ? n - ring : 0; i < n; ++i) mbar_wait(full + 8 * (i % ring), (i / ring) & 1, p.err);
+    } else if (warp == 1 || warp == 3) {
+      // ---- products, each by a converged warp: warp 1 the scores, warp 3 the outputs
       const uint32_t lead = elect_one();
       // the warp stays together when a wait gives up
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err)) != 0;
+        ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, p.err)) != 0;
       };
-      constexpr uint32_t id_s = idesc_fmt0(128, kKeys), id_o = idesc_fmt0(128, D);
-      const uint32_t tm = uniform(tmem), q0 = uniform(desc_lo(sm + S::q));
-      int ks = 0, vs = 0;                                 // next K stage and V block of the rings
-      uint32_t kph = 0, vph = 0, qph = 0, pph = 0;        // phases; pph: bit i of lane i
-      // scores of lane i: query tile at a0, K stage at b0
-      auto scores = [&](int i, uint32_t a0, uint32_t b0) {
-        if (!ok) return;
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            umma_f8(lead, tm + i * 128, a0 + ((term * S::q_half + (kk >> 1) * 8192) >> 4) + 2 * (kk & 1),
-                    b0 + (((kk >> 1) * 8192) >> 4) + 2 * (kk & 1), id_s, (term | kk) != 0 ? 1u : 0u);
-        umma_commit_if(lead, sfull + 8 * i);
-      };
-      // output of lane i: += P V over the unit's one or two blocks at b[]
-      // (the blocks are free after it when `ve` is given; no commit follows the output's own, for
-      // which the CTA waits before it ends)
-      auto output = [&](int i, int n, const uint32_t (&b)[2], uint32_t acc, const uint32_t* ve) {
-        const uint32_t d0 = tm + S::o_col + (S::two ? i * D : 0), a0 = tm + i * 128;
-        wait_all(pfull + 16 * i, (pph >> i) & 1);
-        tc_fence_after();
-        if (ok)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_f16_ts(lead, d0, a0 + kk * 8, b[0] + 2 * kk, id_o, kk == 0 ? acc : 1u);
-        wait_all(pfull + 16 * i + 8, (pph >> i) & 1);
-        tc_fence_after();
-        if (ok && n == 2)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_f16_ts(lead, d0, a0 + 32 + kk * 8, b[1] + 2 * kk, id_o, 1u);
-        if (ok && ve) umma_commit_if(lead, ve[0]);
-        if (ok && ve && n == 2) umma_commit_if(lead, ve[1]);
-        if (ok) umma_commit_if(lead, odone + 8 * i);
-        pph ^= 1u << i;
-      };
-      auto next_k = [&](uint32_t& b0, uint32_t& empty) {
-        wait_all(kfull + 8 * ks, kph);
-        b0 = uniform(desc_lo(sm + S::k + ks * D * kKeys));
-        empty = kempty + 8 * ks;
-        if (++ks == S::nk) {
-          ks = 0;
-          kph ^= 1;
-        }
-      };
-      while (ok && kv8_next(p, w, g)) {
-        const Plan pl = make_plan<D>(p, g);
+      const uint32_t tm = uniform(tmem);
+      uint32_t ph = 0, qph = 0, rph = 0;                  // rph, rs: the ring of K or V
+      int rs = 0;
+      if (warp == 1) {
+        constexpr uint32_t id_s = idesc_fmt0(128, 64);
         constexpr uint32_t kTile = (2 * S::q_half) >> 4;  // from one query tile to the next
-        wait_all(qfull, qph);
-        qph ^= 1;
-        tc_fence_after();
-        uint32_t kb = 0, ke = 0;
-        next_k(kb, ke);
-        scores(0, q0, kb);
-        if (pl.tiles) {
-          scores(1, q0 + kTile, kb);
-        } else if (pl.units > 1) {
-          if (ok) umma_commit_if(lead, ke);
-          next_k(kb, ke);
-          scores(1, q0, kb);
-        }
-        if (ok) umma_commit_if(lead, ke);
-        for (int u = 0; u < pl.units && ok; ++u) {
-          const int n = min(2, g.n - 2 * u);
-          uint32_t vb[2] = {0, 0}, ve[2] = {0, 0};
+        const uint32_t q0 = uniform(desc_lo(sm + S::q)), k0 = uniform(desc_lo(sm + S::k));
+        while (ok && kv8_next(p, w, g)) {
+          const Plan pl = make_plan<D>(p, g);
+          const int steps = pl.steps[0] + pl.steps[1];
+          wait_all(qfull, qph);
+          qph ^= 1;
+          for (int t = 0; t < steps && ok; ++t) {
+            const int i = t & 1, k = t >> 1, buf = 2 * i + (k & 1);
+            if (!pl.tiles || i == 0) wait_all(kfull + 8 * rs, rph);
+            // the buffer's last weights have been used
+            if (k >= 2) wait_all(odone + 8 * buf, buf_parity(ph, i, k - 2));
+            tc_fence_after();
+            if (!ok) break;
+            const uint32_t a0 = q0 + (pl.tiles && i ? kTile : 0), b0 = k0 + rs * (D * 64 >> 4);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (c < n) {
-              wait_all(vfull + 8 * vs, vph);
-              vb[c] = uniform(desc_lo(sm + S::v16 + vs * D * 128));
-              ve[c] = vempty + 8 * vs;
-              if (++vs == S::nv) {
-                vs = 0;
-                vph ^= 1;
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                umma_f8(lead, tm + buf * 64, a0 + ((term * S::q_half + (kk >> 1) * 8192) >> 4) + 2 * (kk & 1),
+                        b0 + (((kk >> 1) * 4096) >> 4) + 2 * (kk & 1), id_s, (term | kk) != 0 ? 1u : 0u);
+            if (!pl.tiles || i == 1) {
+              umma_commit_if(lead, kempty + 8 * rs);
+              if (++rs == S::nk) {
+                rs = 0;
+                rph ^= 1;
               }
             }
-          const bool more = u + (pl.tiles ? 1 : 2) < pl.units;
-          if (more) next_k(kb, ke);
-          if (pl.tiles) {
-            const uint32_t acc = u == 0 ? 0u : 1u;
-            output(0, n, vb, acc, nullptr);
-            if (more) scores(0, q0, kb);
-            output(1, n, vb, acc, ve);
-            if (more) scores(1, q0 + kTile, kb);
-          } else {
-            const int i = u & 1;
-            const uint32_t acc = u < (S::two ? 2 : 1) ? 0u : 1u;
-            output(i, n, vb, acc, ve);
-            if (more) scores(i, q0, kb);
+            umma_commit_if(lead, sfull + 8 * buf);
           }
-          if (ok && more) umma_commit_if(lead, ke);
+          ph = next_phases(ph, pl);
+        }
+      } else {
+        constexpr uint32_t id_o = idesc_fmt0(128, D);
+        const uint32_t v0 = uniform(desc_lo(sm + S::v16));
+        while (ok && kv8_next(p, w, g)) {
+          const Plan pl = make_plan<D>(p, g);
+          const int steps = pl.steps[0] + pl.steps[1];
+          for (int t = 0; t < steps && ok; ++t) {
+            const int i = t & 1, k = t >> 1, buf = 2 * i + (k & 1);
+            if (!pl.tiles || i == 0) wait_all(vfull + 8 * rs, rph);
+            wait_all(pfull + 8 * buf, buf_parity(ph, i, k));
+            tc_fence_after();
+            if (!ok) break;
+            const uint32_t acc = (S::two ? k : t) == 0 ? 0u : 1u, b0 = v0 + rs * (D * 128 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts(lead, tm + S::o_col + (S::two ? i * D : 0), tm + buf * 64 + kk * 8, b0 + 2 * kk, id_o,
+                          kk == 0 ? acc : 1u);
+            if (!pl.tiles || i == 1) {
+              umma_commit_if(lead, vempty + 8 * rs);
+              if (++rs == S::nv) {
+                rs = 0;
+                rph ^= 1;
+              }
+            }
+            // (no commit follows the last output's own, for which the CTA waits before it ends)
+            umma_commit_if(lead, odone + 8 * buf);
+          }
+          ph = next_phases(ph, pl);
         }
       }
     }
@@ -347,12 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (kv8_next(p, w, g)) {
       for (int j = 0; j < g.n; ++j, ++vt) {
         const int r = vt % S::nv;
-        ok = ok && mbar_wait(rfull + 8 * r, (vt / S::nv) & 1, p.err);
-        ok = ok && (vt < S::nv || mbar_wait(vempty + 8 * r, (vt / S::nv - 1) & 1, p.err));
+        ok = ok && wait_for(rfull + 8 * r, (vt / S::nv) & 1, p.err);
+        ok = ok && (vt < S::nv || wait_for(vempty + 8 * r, (vt / S::nv - 1) & 1, p.err));
         if (ok) {
           const uint8_t* src = smem + S::v8 + r * D * 64;
           uint8_t* dst = smem + S::v16 + r * D * 128;
-#pragma unroll 4
+#pragma unroll 2
           for (int i = tid; i < D * 4; i += 128) {
             const int d = i >> 2, c = i & 3;
             const uint4 x = *reinterpret_cast<const uint4*>(src + d * 64 + ((c ^ ((d >> 1) & 3)) << 4));
@@ -379,11 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    constexpr int kCols = S::two ? kKeys : kKeys / 2;     // keys of a unit a thread takes
     const int grp = (warp - 4) >> 2, qd = warp & 3, r = qd * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(qd * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + S::xch);
-    int step[2] = {0, 0};                                 // S buffers (lanes) consumed so far
+    uint32_t ph = 0;
     while (kv8_next(p, w, g)) {
       const Plan pl = make_plan<D>(p, g);
       const int left = g.row.cnt * p.group - g.tile * S::rows;      // rows from the tile's first on
@@ -396,39 +414,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kQ = S::two ? D : D / 2;
         const int d0 = S::two ? 0 : grp * kQ;
         const bool load = S::two ? (pl.tiles || grp == 0) : true;
-        const __nv_bfloat16* q = p.q + g.b * p.q_st[0] + (row / p.group) * p.q_st[1] +
-                                 (g.head * p.group + row % p.group) * p.q_st[2] + d0;
-        uint4 x[kQ / 8];
+        const __nv_bfloat16* q = p.q + g.b * p.q_st[0] + p.by_group.div(row) * p.q_st[1] +
+                                 (g.head * p.group + p.by_group.mod(row)) * p.q_st[2] + d0;
+        // the largest magnitude (a second group on the same rows needs it for the row's factor)
         float am = 0.0f;
-        // the second group of a one-tile segment needs the row's factor only, from the same values
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < kQ / 8; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (row_ok && d0 + i * 8 < p.c.D) x[i] = *reinterpret_cast<const uint4*>(q + i * 8);
-          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (row_ok && d0 + i * 8 < p.c.D) x = *reinterpret_cast<const uint4*>(q + i * 8);
+          const uint32_t v[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float a = fabsf(__uint_as_float(v[c] << 16)), b = fabsf(__uint_as_float(v[c] & 0xffff0000u));
-            am = fmaxf(am, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
+          for (int c = 0; c < 4; ++c) {                   // bf16 bits order like their values; not finite: left out
+            const uint32_t a = v[c] & 0xffffu, b = v[c] >> 16;
+            am = fmaxf(am, __uint_as_float(a < 0x7f80u ? a << 16 : 0u));
+            am = fmaxf(am, __uint_as_float(b < 0x7f80u ? b << 16 : 0u));
           }
         }
-        if (!S::two) {
+        if (!S::two) {                                    // over both halves of the row
           xch[grp * 128 + r] = am;
-          named_bar_sync(1 + qd, 64);
+          named_bar_sync(11 + qd, 64);
           am = fmaxf(am, xch[(grp ^ 1) * 128 + r]);
-          named_bar_sync(1 + qd, 64);
+          named_bar_sync(11 + qd, 64);
         }
         const int e = am > 0.0f ? min(max(exp_of(am) - 7, -118), 120) : 0;
         const float inv = exp2i(-e);
         rowf *= exp2i(e);
         if (load) {
           uint8_t* dst = smem + S::q + (pl.tiles ? grp * 2 * S::q_half : 0) + r * 64;
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < kQ / 16; ++i) {             // 16 dims: one 16-byte chunk of each term
+            uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (row_ok && d0 + i * 16 < p.c.D) {
+              x[0] = *reinterpret_cast<const uint4*>(q + i * 16);
+              x[1] = *reinterpret_cast<const uint4*>(q + i * 16 + 8);
+            }
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 y = x[2 * i + (c >> 1)];
+              const uint4 y = x[c >> 1];
               const uint32_t v0 = (c & 1) ? y.z : y.x, v1 = (c & 1) ? y.w : y.y;
               float f[4] = {__uint_as_float(v0 << 16) * inv, __uint_as_float(v0 & 0xffff0000u) * inv,
                             __uint_as_float(v1 << 16) * inv, __uint_as_float(v1 & 0xffff0000u) * inv};
@@ -454,160 +477,168 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       int lo, hi, lo_last, hi_first, t0, t1;
-      kv8_seen(p, g.row, row / p.group, lo, hi);
-      kv8_seen(p, g.row, r0 / p.group, t0, hi_first);
-      kv8_seen(p, g.row, (r0 + max(rows, 1) - 1) / p.group, lo_last, t1);
+      kv8_seen(p, g.row, p.by_group.div(row), lo, hi);
+      kv8_seen(p, g.row, p.by_group.div(r0), t0, hi_first);
+      kv8_seen(p, g.row, p.by_group.div(r0 + max(rows, 1) - 1), lo_last, t1);
       const float4* scales = p.c.scale +
-          ((static_cast<size_t>(p.layer) * p.c.n_slots + g.row.slot) * p.c.n_kv + g.head) * p.c.nblk;
-      const int last_blk = g.blk + g.n - 1;
-      const int u_step = S::two && !pl.tiles ? 2 : 1;
-      int u = S::two && !pl.tiles ? grp : 0;
-      float4 sc[2];                                       // scales of the next unit's blocks
-      auto load_scales = [&](int unit) {
-        const int b = g.blk + 2 * unit;
-        if (S::two) {
-          sc[0] = __ldg(scales + min(b, last_blk));
-          sc[1] = __ldg(scales + min(b + 1, last_blk));
-        } else {
-          sc[0] = __ldg(scales + min(b + grp, last_blk));
+          ((static_cast<size_t>(p.layer) * p.c.n_slots + g.row.slot) * p.c.n_kv + g.head) * p.c.nblk + g.blk;
+      const int steps = pl.steps[grp];
+      const int stride = pl.tiles ? 1 : 2, first = pl.tiles ? 0 : grp;   // block of step k: first + k * stride
+      auto scale_of = [&](int k) { return __ldg(scales + min(first + k * stride, g.n - 1)); };
+      float4 sc = scale_of(0);
+      float m = -INFINITY, l = 0.0f;
+      auto load = [&](int k, float (&x)[64]) {            // the scores of step k, in flight
+        ok = ok && wait_for(sfull + 8 * (2 * grp + (k & 1)), buf_parity(ph, grp, k), p.err);
+        tc_fence_after();
+        const uint32_t ts = tl + (2 * grp + (k & 1)) * 64;
+        tmem_ld32_async(ts, x);
+        tmem_ld32_async(ts + 32, x + 32);
+      };
+      // moves the row's reference to nm, and with it l and (if it has begun) this warp's rows of O:
+      // after the last product on them
+      auto move_to = [&](float nm, int k, int j) {
+        const float f = nm == m ? 1.0f : exp2_approx(m - nm);
+        m = nm;
+        l *= f;
+        const int before = S::two ? k - 1 : (j - 1) >> 1, of = S::two ? grp : grp ^ 1;
+        if ((S::two ? k : j) > 0) {
+          ok = ok && wait_for(odone + 8 * (2 * of + (before & 1)), buf_parity(ph, of, before), p.err);
+          tc_fence_after();
+          const uint32_t to = tl + S::o_col + (S::two ? grp * D : 0);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float y[32];
+            tmem_ld32_async(to + c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] *= f;
+            tmem_st32_async(to + c, reinterpret_cast<uint32_t*>(y));
+          }
+          tmem_wait_st();
         }
       };
-      load_scales(min(u, pl.units - 1));
-      float m = -INFINITY, l = 0.0f;
-      bool begun = false;                                 // this output holds something
-      int buf = S::two ? grp : 0;
-      for (; u < pl.units; u += u_step) {
-        if (!S::two) buf = u & 1;
-        ok = ok && mbar_wait(sfull + 8 * buf, step[buf] & 1, p.err);
-        tc_fence_after();
-        float x[kCols];
-        const uint32_t ts = tl + buf * 128 + (S::two ? 0 : grp * 64);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) tmem_ld32_async(ts + c, x + c);
-        float gk[S::two ? 2 : 1], fv[S::two ? 2 : 1], un[S::two ? 2 : 1];
-#pragma unroll
-        for (int i = 0; i < (S::two ? 2 : 1); ++i) {
-          gk[i] = rowf * sc[i].x;
-          const int ev = exp_of(sc[i].y);
-          fv[i] = static_cast<float>(ev);
-          un[i] = exp2i(-ev);
-        }
-        load_scales(min(u + u_step, pl.units - 1));
-        const int key0 = (g.blk + 2 * u) * kKv8Block + (S::two ? 0 : grp * 64);
+      float x[64];
+      if (steps > 0) load(0, x);
+      for (int k = 0; k < steps; ++k) {
+        const int buf = 2 * grp + (k & 1), j = first + k * stride, key0 = (g.blk + j) * kKv8Block;
+        const float gk = fmaxf(rowf * sc.x, FLT_MIN);       // (never 0: a masked score stays -infinity)
+        const int ev = exp_of(sc.y);
+        const float fv = static_cast<float>(ev), un = exp2i(-ev);
+        sc = scale_of(k + 1);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) asm volatile("" : "+f"(x[c]));   // not used before the wait
-        if (key0 < lo_last || key0 + kCols > hi_first) {
+        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(x[c]));   // not used before the wait
+        if (__builtin_expect(key0 < lo_last || key0 + 64 > hi_first, 0)) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
+          for (int c = 0; c < 64; ++c)
             if (c < lo - key0 || c >= hi - key0) x[c] = -INFINITY;
         }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kCols / 64; ++i) {
-          float h[4] = {x[64 * i], x[64 * i + 1], x[64 * i + 2], x[64 * i + 3]};
+        // the block's largest score. (-infinity times gk stays -infinity: gk > 0)
+        auto largest = [&]() {
+          float h[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
           for (int c = 4; c < 60; c += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = max3(h[k], x[64 * i + c + k], x[64 * i + c + 4 + k]);
+            for (int i = 0; i < 4; ++i) h[i] = max3(h[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) h[k] = fmaxf(h[k], x[64 * i + 60 + k]);
-          mx = fmaxf(mx, fmaf(fmaxf(fmaxf(h[0], h[1]), fmaxf(h[2], h[3])), gk[i], fv[i]));
-        }
-        if (!S::two) {                                    // the row's maximum over both halves
-          xch[((u & 1) * 2 + grp) * 128 + r] = mx;
-          named_bar_sync(1 + qd, 64);
-          mx = fmaxf(mx, xch[((u & 1) * 2 + (grp ^ 1)) * 128 + r]);
-        }
-        const bool move = mx > m + 8.0f || (m == -INFINITY && mx > m);
-        if (__any_sync(0xffffffffu, move)) {
-          const float nm = move ? mx : m;
-          const float k = nm == m ? 1.0f : exp2_approx(m - nm);
-          m = nm;
-          l *= k;
-          if (begun) {                                    // rescale this warp's rows of O
-            const int ob = S::two ? buf : (u - 1) & 1;
-            ok = ok && mbar_wait(odone + 8 * ob, (step[ob] - 1) & 1, p.err);
-            tc_fence_after();
-            const uint32_t to = tl + S::o_col + (S::two ? grp * D : grp * (D / 2));
-#pragma unroll 1
-            for (int c = 0; c < (S::two ? D : D / 2); c += 32) {
-              float y[32];
-              tmem_ld32_async(to + c, y);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] *= k;
-              tmem_st32_async(to + c, reinterpret_cast<uint32_t*>(y));
-            }
-            tmem_wait_st();
+          for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[60 + i]);
+          return fmaf(max3(h[0], h[1], fmaxf(h[2], h[3])), gk, fv);
+        };
+        auto passes = [&](float mx) { return mx > m + kLag || (m == -INFINITY && mx > m); };
+        if (!S::two) {
+          // the reference of the block before comes from the other group, this block's goes to it
+          const float mx = largest();
+          if (j > 0) {
+            named_bar_sync(1 + (grp ^ 1) * 4 + qd, 64);
+            const float old = xch[((j - 1) & 1) * 128 + r];
+            if (old != m) l *= exp2_approx(m - old);      // (m = -infinity: l is 0)
+            m = old;
           }
+          const bool move = passes(mx);
+          if (j + 1 < g.n) {
+            xch[(j & 1) * 128 + r] = move ? mx : m;
+            asm volatile("bar.arrive %0, 64;" ::"r"(1 + grp * 4 + qd) : "memory");
+          }
+          if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) move_to(move ? mx : m, k, j);
         }
-        begun = true;
-        const float base = m == -INFINITY ? 0.0f : kLift - m;
-#pragma unroll
-        for (int i = 0; i < kCols / 64; ++i) {
-          const float off = fv[i] + base;
-          float s0 = 0.0f, s1 = 0.0f;
-          uint32_t pk[32];                                // positions 2 k, 2 k + 1 of the block
+        uint32_t pk[32];                                  // positions 2 i, 2 i + 1 of the block
+        float sum;
+        while (true) {
+          const float off = fv + (m == -INFINITY ? 0.0f : kLift - m);
+          float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float a = exp2_approx(fmaf(x[64 * i + c], gk[i], off));
-            const float b = exp2_approx(fmaf(x[64 * i + c + 1], gk[i], off));
-            s0 += a;
-            s1 += b;
-            const __half2 h2 = __floats2half2_rn(a, b);
-            // tokens 8 h + 2 t, + 1 of a 16-token group stand at positions 4 t + 2 h, + 1
-            const int k = (c >> 4) * 8 + ((c >> 1) & 3) * 2 + ((c >> 3) & 1);
-            pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
+            const float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(gk, gk), make_float2(off, off));
+            const float2 w2 = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            s2 = add2(s2, w2);
+            const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
+            // tokens 16 w + 8 h + 2 t, + 1 stand at positions 16 t + 4 w + 2 h, + 1
+            pk[((c >> 1) & 3) * 8 + (c >> 4) * 2 + ((c >> 3) & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
           }
-          l = fmaf(s0 + s1, un[i], l);
-          const int blk = S::two ? i : grp;
-          tmem_st32_async(tl + buf * 128 + blk * 32, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + 16 * buf + 8 * blk);
+          sum = s2.x + s2.y;
+          if (!S::two) break;
+          // head_dim <= 128: the weights against the reference as it stood, the maximum found
+          // meanwhile; once more if it passes the reference too far (rare after the first block)
+          const float mx = largest();
+          const bool move = passes(mx);
+          if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
+          move_to(move ? mx : m, k, j);
         }
-        ++step[buf];
+        l = fmaf(sum, un, l);
+        tmem_st32_async(tl + buf * 64, pk);
+        if (k + 1 < steps) load(k + 1, x);                // (in flight while the weights are stored)
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull + 8 * buf);
       }
 
-      // ---- the output. One tile on two lanes (head_dim <= 128): group 0 joins both outputs
-      const bool join = S::two && !pl.tiles;
-      if (!S::two) {                     // in the half of xch that the last unit did not use
-        float* x = xch + (pl.units & 1) * 256;
-        x[grp * 128 + r] = l;
-        named_bar_sync(1 + qd, 64);
-        l += x[(grp ^ 1) * 128 + r];
-        named_bar_sync(1 + qd, 64);
-      }
+      // ---- the output
+      const bool join = S::two && !pl.tiles;              // group 0 joins both lanes' outputs
+      const int slot = 2 * blockIdx.x + (g.first ? 0 : 1), tr = row - g.tile * S::rows;
       float k0 = 1.0f, k1 = 0.0f;
-      bool have1 = false;
       if (join) {
-        if (grp == 1) {
-          xch[r] = m;
-          xch[128 + r] = l;
-        }
-        named_bar_sync(5, 256);
+        float2* x = reinterpret_cast<float2*>(xch);
+        if (grp == 1) x[r] = make_float2(m, l);
+        named_bar_sync(9, 256);
         if (grp == 0) {
-          have1 = pl.units > 1;
-          const float m1 = xch[r], l1 = xch[128 + r];
-          const float mm = fmaxf(m, m1);
+          const float2 y = x[r];
+          const float mm = fmaxf(m, y.x);
           k0 = m == -INFINITY ? 1.0f : exp2_approx(m - mm);
-          k1 = m1 == -INFINITY ? 1.0f : exp2_approx(m1 - mm);
-          l = l * k0 + l1 * k1;
+          k1 = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - mm);
+          l = l * k0 + y.y * k1;
           m = mm;
-          if (have1) ok = ok && mbar_wait(odone + 8, (step[1] + pl.units / 2 - 1) & 1, p.err);
         }
+      } else if (!S::two) {
+        named_bar_sync(10, 256);         // no reference in xch is read any more
+        float2* x = reinterpret_cast<float2*>(xch);
+        x[grp * 128 + r] = make_float2(m, l);
+        named_bar_sync(10, 256);
+        const float2 y = x[(grp ^ 1) * 128 + r];
+        const float mm = fmaxf(m, y.x);  // the last block's, which the output is relative to
+        l = l * (m == -INFINITY ? 1.0f : exp2_approx(m - mm)) + y.y * (y.x == -INFINITY ? 1.0f : exp2_approx(y.x - mm));
+        m = mm;
       }
       if (!join || grp == 0) {
-        const int ob = S::two ? buf : (pl.units - 1) & 1;
-        ok = ok && mbar_wait(odone + 8 * ob, (step[ob] - 1) & 1, p.err);
+        // the last products on the outputs read here. A wait may look one phase ahead only, so the
+        // groups of head_dim 256 wait for the last two blocks in order.
+        if (S::two) {
+          ok = ok && wait_for(odone + 8 * (2 * grp + ((steps - 1) & 1)), buf_parity(ph, grp, steps - 1), p.err);
+          if (join && pl.steps[1] > 0) {
+            const int e = pl.steps[1] - 1;
+            ok = ok && wait_for(odone + 8 * (2 + (e & 1)), buf_parity(ph, 1, e), p.err);
+          }
+        } else {
+          for (int t = max(0, g.n - 2); t < g.n; ++t)
+            ok = ok && wait_for(odone + 8 * (2 * (t & 1) + ((t >> 1) & 1)), buf_parity(ph, t & 1, t >> 1), p.err);
+        }
         tc_fence_after();
-        const float norm = g.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-        const int qi = row / p.group, qh = g.head * p.group + row % p.group;
-        const int slot = 2 * blockIdx.x + (g.first ? 0 : 1), tr = row - g.tile * S::rows;
+        const bool have1 = join && pl.steps[1] > 0;
+        const float norm = l == 0.0f ? 0.0f : 1.0f / l;
+        const int qi = p.by_group.div(row), qh = g.head * p.group + p.by_group.mod(row);
         __nv_bfloat16* dst = p.out + g.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2];
-        float* ws = p.ws + (static_cast<size_t>(slot) * S::rows + tr) * D;
+        // a part's outputs: [D / 4][rows][4], so that neighbouring rows are neighbours
+        float4* ws = reinterpret_cast<float4*>(p.ws + static_cast<size_t>(slot) * S::rows * D) + tr;
         const int c_from = S::two ? 0 : grp * (D / 2), c_to = S::two ? D : c_from + D / 2;
 #pragma unroll 1
         for (int c = c_from; c < c_to; c += 32) {
@@ -621,21 +652,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) y[i] = fmaf(z[i], k1, y[i] * k0);
           } else {
             tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(y[i]));
           }
           if (row_ok && !g.whole) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(ws + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              ws[(c + i) / 4 * S::rows] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
           } else if (row_ok && c < p.c.D) {
+            uint32_t o[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t o[4];
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i] * norm, y[2 * i + 1] * norm);
+              o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+              st_global_32(dst + c, o);
+              st_global_32(dst + c + 16, o + 8);
+            } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(y[i + 2 * k] * norm, y[i + 2 * k + 1] * norm);
-                o[k] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(dst + c + 2 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
         }
@@ -647,12 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
       }
-      if (join) {
-        named_bar_sync(5, 256);          // group 1 keeps its output and Q until group 0 has read them
-      }
-      if (S::two && !pl.tiles && grp == 0) step[1] += pl.units / 2;
-      if (S::two && !pl.tiles && grp == 1) step[0] += (pl.units + 1) / 2;
-      if (S::two && pl.tiles) step[grp ^ 1] += pl.units;
+      // group 1 keeps its output and Q until group 0 has read them; at head_dim 256 neither group
+      // goes on to a new output, Q or exchange before the other has read
+      if (join || !S::two) named_bar_sync(join ? 9 : 10, 256);
+      ph = next_phases(ph, pl);
     }
   }
 
@@ -665,22 +700,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-static cudaError_t launch_tc(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
-                             cudaStream_t s) {
+static cudaError_t launch_tc(const Kv8AttendParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Tc<D>::total;
   cfg.stream = s;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_attend_tc_kernel<D>, tm_k, tm_v, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_attend_tc_kernel<D>, p);
   return e != cudaSuccess ? e : launch_kv8_merge(p, s);
 }
 
-cudaError_t launch_kv8_attend_tc(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Kv8AttendParams& p,
-                                 cudaStream_t s) {
-  if (p.c.Ds == 64) return launch_tc<64>(tm_k, tm_v, p, s);
-  if (p.c.Ds == 128) return launch_tc<128>(tm_k, tm_v, p, s);
-  return launch_tc<256>(tm_k, tm_v, p, s);
+cudaError_t launch_kv8_attend_tc(const Kv8AttendParams& p, cudaStream_t s) {
+  if (p.c.Ds == 64) return launch_tc<64>(p, s);
+  if (p.c.Ds == 128) return launch_tc<128>(p, s);
+  return launch_tc<256>(p, s);
 }
 
 template <int D>

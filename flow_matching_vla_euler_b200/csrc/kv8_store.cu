@@ -74,9 +74,11 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return quant4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-// Word index of (dim d, token quad tg) in the transposing tile: the 32 lanes of a store have
+// Word index of (dim d, word of its row) in the transposing tile: the 32 lanes of a store have
 // dims 8 apart, which the exclusive or spreads over all banks.
-__device__ __forceinline__ int vt_word(int d, int tg) { return (d * 16 + tg) ^ ((d >> 3) & 31); }
+__device__ __forceinline__ int vt_word(int d, int word) { return (d * 16 + word) ^ ((d >> 3) & 31); }
+// Token quad tg (2t, 2t+1, 2t+8, 2t+9 of the 16-token group w = tg / 4, t = tg % 4) is word 4t + w.
+__device__ __forceinline__ int quad_word(int tg) { return 4 * (tg & 3) + (tg >> 2); }
 
 }  // namespace
 
@@ -152,12 +154,12 @@ __global__ void __launch_bounds__(2 * D) kv8_write_kernel(const Kv8RowsParams p)
       q.x = quant4(bf_lo(x[i].x) * inv, bf_hi(x[i].x) * inv, bf_lo(x[i].y) * inv, bf_hi(x[i].y) * inv);
       q.y = quant4(bf_lo(x[i].z) * inv, bf_hi(x[i].z) * inv, bf_lo(x[i].w) * inv, bf_hi(x[i].w) * inv);
       if (broken[tok]) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      *reinterpret_cast<uint2*>(blk + (vec >> 3) * 4096 + tok * 64 + (vec & 7) * 8) = q;
+      *reinterpret_cast<uint2*>(blk + (vec >> 3) * 4096 + kv8_chunk(tok, (vec & 7) >> 1) + (vec & 1) * 8) = q;
     }
     if (rescale)
       for (int i = tid; i < u.lo * kVec; i += D) {
         const int tok = i / kVec, v = i % kVec;
-        uint2* a = reinterpret_cast<uint2*>(blk + (v >> 3) * 4096 + tok * 64 + (v & 7) * 8);
+        uint2* a = reinterpret_cast<uint2*>(blk + (v >> 3) * 4096 + kv8_chunk(tok, (v & 7) >> 1) + (v & 1) * 8);
         const uint2 w = *a;
         *a = make_uint2(rescale4(w.x, fold), rescale4(w.y, fold));
       }
@@ -181,33 +183,32 @@ __global__ void __launch_bounds__(2 * D) kv8_write_kernel(const Kv8RowsParams p)
           c[i] = bf_hi(w) * inv;
         }
         const int d = vec * 8 + 2 * d2;
-        vt[vt_word(d, tg)] = quant4(a[0], a[1], a[2], a[3]) & keep;
-        vt[vt_word(d + 1, tg)] = quant4(c[0], c[1], c[2], c[3]) & keep;
+        vt[vt_word(d, quad_word(tg))] = quant4(a[0], a[1], a[2], a[3]) & keep;
+        vt[vt_word(d + 1, quad_word(tg))] = quant4(c[0], c[1], c[2], c[3]) & keep;
       }
     }
     named_bar_sync(1, D);
-    for (int i = tid; i < D * 4; i += D) {               // 16-byte pieces (dim, 16-token group)
-      const int d = i >> 2, w = i & 3;
-      const int t0 = 16 * w;
-      if (t0 >= u.hi || (t0 + 16 <= u.lo && !rescale)) continue;
-      uint32_t y[4];
+    const bool whole = u.lo == 0 && u.hi == kKv8Block;
+    for (int i = tid; i < D * 4; i += D) {               // 16-byte pieces (dim, t): tokens 16w + 8h + 2t + e
+      const int d = i >> 2, t = i & 3;
+      uint32_t y[4], m[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) y[t] = vt[vt_word(d, 4 * w + t)];
-      uint4* a = reinterpret_cast<uint4*>(blk + d * 64 + t0);
-      if (t0 < u.lo || t0 + 16 > u.hi) {                 // a ragged group keeps its other tokens
+      for (int w = 0; w < 4; ++w) {
+        y[w] = vt[vt_word(d, 4 * t + w)];
+        m[w] = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int tok = 16 * w + 8 * (c >> 1) + 2 * t + (c & 1);
+          if (tok >= u.lo && tok < u.hi) m[w] |= 0xffu << (8 * c);
+        }
+      }
+      if (!whole && !rescale && !(m[0] | m[1] | m[2] | m[3])) continue;
+      uint4* a = reinterpret_cast<uint4*>(blk + kv8_chunk(d, t));
+      if (!whole) {                                      // a ragged block keeps its other tokens
         const uint4 old4 = *a;
         const uint32_t old[4] = {old4.x, old4.y, old4.z, old4.w};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int tok = t0 + 8 * (c >> 1) + 2 * t + (c & 1);
-            if (tok >= u.lo && tok < u.hi) m |= 0xffu << (8 * c);
-          }
-          const uint32_t o = rescale ? rescale4(old[t], fold) : old[t];
-          y[t] = (y[t] & m) | (o & ~m);
-        }
+        for (int w = 0; w < 4; ++w) y[w] = (y[w] & m[w]) | ((rescale ? rescale4(old[w], fold) : old[w]) & ~m[w]);
       }
       *a = make_uint4(y[0], y[1], y[2], y[3]);
     }
@@ -237,23 +238,23 @@ __global__ void __launch_bounds__(2 * D) kv8_read_kernel(const Kv8RowsParams p) 
       const int tok = 16 * (tg >> 2) + 8 * (c >> 1) + 2 * (tg & 3) + (c & 1);
       q[i] = make_uint2(0, 0);
       if (tok >= u.lo && tok < u.hi)
-        q[i] = *reinterpret_cast<const uint2*>(blk + (vec >> 3) * 4096 + tok * 64 + (vec & 7) * 8);
+        q[i] = *reinterpret_cast<const uint2*>(blk + (vec >> 3) * 4096 + kv8_chunk(tok, (vec & 7) >> 1) + (vec & 1) * 8);
     }
   } else {
     for (int i = tid; i < D * 4; i += D) {
-      const int d = i >> 2, w = i & 3;
-      const uint4 y = *reinterpret_cast<const uint4*>(blk + d * 64 + 16 * w);
-      vt[vt_word(d, 4 * w)] = y.x;
-      vt[vt_word(d, 4 * w + 1)] = y.y;
-      vt[vt_word(d, 4 * w + 2)] = y.z;
-      vt[vt_word(d, 4 * w + 3)] = y.w;
+      const int d = i >> 2, t = i & 3;
+      const uint4 y = *reinterpret_cast<const uint4*>(blk + kv8_chunk(d, t));
+      vt[vt_word(d, 4 * t)] = y.x;
+      vt[vt_word(d, 4 * t + 1)] = y.y;
+      vt[vt_word(d, 4 * t + 2)] = y.z;
+      vt[vt_word(d, 4 * t + 3)] = y.w;
     }
     named_bar_sync(1, D);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       uint32_t w[8];
 #pragma unroll
-      for (int d = 0; d < 8; ++d) w[d] = vt[vt_word(vec * 8 + d, tg0 + 8 * g)];
+      for (int d = 0; d < 8; ++d) w[d] = vt[vt_word(vec * 8 + d, quad_word(tg0 + 8 * g))];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {        // byte c of the eight words
         const uint32_t sel = 0x0040u + 0x0011u * c;
