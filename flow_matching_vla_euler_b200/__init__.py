@@ -496,6 +496,8 @@ class KVCache8:
         self.capacity, self.n_slots = int(capacity), int(n_slots)
         self.handle = vla_kv8_create(c)
         self.device = torch.cuda.current_device()
+        # the calls' argument structs, filled anew by each call (a handle is one thread's)
+        self._args = vla_kv8_rows(), vla_kv8_query()
 
     def close(self):
         if getattr(self, "handle", None):
@@ -508,15 +510,18 @@ class KVCache8:
         except Exception:
             pass
 
-    # ---- argument checks: the library sees pointers only
+    # ---- argument checks: the library sees pointers only. One fast test each; what fails it is
+    # looked at again for its message.
 
     def _index(self, t, batch, name):
         if t is None:
             return None
         import torch
-        _expect(t, (batch,), name, torch.int32)
-        self._here(t, name)
-        return _dev_ptr(t, 4)
+        if not (t.dtype is torch.int32 and t.shape == (batch,) and t.get_device() == self.device
+                and t.is_contiguous()):
+            _expect(t, (batch,), name, torch.int32)
+            self._here(t, name)
+        return _dev_ptr(t, 4) if not t.is_contiguous() else t.data_ptr()
 
     def _here(self, t, name):
         if not t.is_cuda:
@@ -525,28 +530,31 @@ class KVCache8:
             raise ValueError(f"{name}: on {t.device}, the cache is on cuda:{self.device}")
 
     def _strided(self, t, shape, name):
-        """Pointer and the strides of all dims but the last, which must be dense (several
-        trailing dims in one, where ``shape`` joins them)."""
-        _expect(t, shape, name)
-        self._here(t, name)
+        """Pointer and the strides of all dims but the last, which must be dense; (0, 0, 0) for a
+        packed tensor."""
         import torch
-        if t.dtype not in (torch.bfloat16, torch.int16):
+        if not (t.shape == shape and t.get_device() == self.device
+                and (t.dtype is torch.bfloat16 or t.dtype is torch.int16)):
+            _expect(t, shape, name)
+            self._here(t, name)
             raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 (or its bits in int16)")
+        if t.is_contiguous():
+            return t.data_ptr(), _PACKED
         st = t.stride()
-        # the stride of a dim of one element (or of the last) says nothing: any value will do
-        if t.shape[-1] > 1 and st[-1] != 1:
+        # the stride of a dim of one element says nothing: any value will do
+        if shape[-1] > 1 and st[-1] != 1:
             raise ValueError(f"{name}: the last dim must be dense")
-        st = [s if n > 1 else 8 for s, n in zip(st[:-1], shape[:-1])]
+        st = tuple(s if n > 1 else 8 for s, n in zip(st[:-1], shape[:-1]))
         if not any(st):
             raise ValueError(f"{name}: every dim is expanded (all strides 0)")
         return t.data_ptr(), st
 
     def _rows(self, batch, n_tokens, layer, n_layers, pos, count, slots, strides):
-        r = vla_kv8_rows()
+        r = self._args[0]
         r.slots = self._index(slots, batch, "slots")
         r.pos = self._index(pos, batch, "pos")
         r.count = self._index(count, batch, "count")
-        r.layer, r.n_layers, r.batch, r.n_tokens = int(layer), int(n_layers), int(batch), int(n_tokens)
+        r.layer, r.n_layers, r.batch, r.n_tokens = layer, n_layers, batch, n_tokens
         r.stride[:] = strides
         return r
 
@@ -557,13 +565,16 @@ class KVCache8:
         pos[b] stay, those behind the written ones are gone."""
         if K.dim() != 4:
             raise ValueError("K: expected [layers, batch, n_tokens, n_kv_heads * head_dim]")
-        n, batch, n_tok = (int(d) for d in K.shape[:3])
+        n, batch, n_tok, _ = K.shape
         shape = (n, batch, n_tok, self.n_kv_heads * self.head_dim)
         kp, ks = self._strided(K, shape, "K")
         vp, vs = self._strided(V, shape, "V")
-        if ks != vs:
-            raise ValueError(f"K and V: strides {ks} and {vs}, expected the same")
-        vla_kv8_write(self.handle, kp, vp, self._rows(batch, n_tok, layer, n, pos, count, slots, ks), _stream())
+        if ks != vs:                     # one packed, one not: the packed one's strides in full
+            ks, vs = _full_strides(K, ks), _full_strides(V, vs)
+            if ks != vs:
+                raise ValueError(f"K and V: strides {ks} and {vs}, expected the same")
+        vla_kv8_write(self.handle, kp, vp, self._rows(batch, n_tok, int(layer), n, pos, count, slots, ks),
+                      _raw_stream(self.device))
 
     def read(self, n_tokens: int, pos=None, count=None, slots=None, layer: int = 0, n_layers=None, batch=None,
              K_out=None, V_out=None):
@@ -571,16 +582,16 @@ class KVCache8:
         bits as Expert.set_prefix takes them unless K_out and V_out are given. Row b gets count[b]
         tokens (n_tokens) from position pos[b] (0) of slot slots[b] (b); the output behind them is
         left as it was (zeros in a tensor made here)."""
-        import torch
         n = self.n_layers - int(layer) if n_layers is None else int(n_layers)
         if batch is None:
             given = [t for t in (K_out[0] if K_out is not None and K_out.dim() else None, slots, pos, count)
                      if t is not None]
-            batch = int(given[0].shape[0]) if given else self.n_slots
+            batch = given[0].shape[0] if given and given[0].dim() else self.n_slots
         shape = (n, int(batch), int(n_tokens), self.n_kv_heads * self.head_dim)
         if (K_out is None) != (V_out is None):
             raise ValueError("K_out and V_out go together")
         if K_out is None:
+            import torch
             if min(shape) < 1:
                 raise ValueError(f"K, V: no such shape {shape}")
             dev = torch.device("cuda", self.device)
@@ -590,8 +601,11 @@ class KVCache8:
         kp, ks = self._strided(K_out, shape, "K_out")
         vp, vs = self._strided(V_out, shape, "V_out")
         if ks != vs:
-            raise ValueError(f"K_out and V_out: strides {ks} and {vs}, expected the same")
-        vla_kv8_read(self.handle, kp, vp, self._rows(batch, n_tokens, layer, n, pos, count, slots, ks), _stream())
+            ks, vs = _full_strides(K_out, ks), _full_strides(V_out, vs)
+            if ks != vs:
+                raise ValueError(f"K_out and V_out: strides {ks} and {vs}, expected the same")
+        vla_kv8_read(self.handle, kp, vp, self._rows(shape[1], shape[2], int(layer), n, pos, count, slots, ks),
+                     _raw_stream(self.device))
         return K_out, V_out
 
     def attend(self, q, kv_len, layer: int = 0, slots=None, q_pos=None, q_count=None, causal: bool = False,
@@ -606,7 +620,7 @@ class KVCache8:
         import torch
         if q.dim() != 4:
             raise ValueError("q: expected [batch, n_q, n_heads, head_dim]")
-        batch, n_q, n_heads = (int(d) for d in q.shape[:3])
+        batch, n_q, n_heads, _ = q.shape
         if scale is not None and not float(scale) > 0.0:
             raise ValueError("scale must be > 0")
         shape = (batch, n_q, n_heads, self.head_dim)
@@ -621,7 +635,7 @@ class KVCache8:
             lp = _dev_ptr(lse, 4)
         if kv_len is None:
             raise ValueError("kv_len is required")
-        a = vla_kv8_query()
+        a = self._args[1]
         a.slots = self._index(slots, batch, "slots")
         a.kv_len = self._index(kv_len, batch, "kv_len")
         a.q_pos = self._index(q_pos, batch, "q_pos")
@@ -631,11 +645,24 @@ class KVCache8:
         a.scale = 0.0 if scale is None else float(scale)
         a.q_stride[:] = qs
         a.out_stride[:] = os_
-        vla_kv8_attend(self.handle, qp, op, lp, a, _stream())
+        vla_kv8_attend(self.handle, qp, op, lp, a, _raw_stream(self.device))
         return out
 
     def status(self):
-        vla_kv8_status(self.handle, _stream())
+        vla_kv8_status(self.handle, _raw_stream(self.device))
+
+
+_PACKED = (0, 0, 0)
+
+
+def _full_strides(t, st):
+    return tuple(s if n > 1 else 8 for s, n in zip(t.stride()[:-1], t.shape[:-1])) if st is _PACKED else st
+
+
+def _raw_stream(device):
+    """torch.cuda.current_stream(device).cuda_stream without the Stream object."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 class Expert:
