@@ -11,14 +11,15 @@
 //               [128, 256), hi = e4m3(q), lo = e4m3(q - hi). Exact for bf16 values above
 //               2^-10 of the largest, else to 2^-17 of it. Two E4M3 products take as long as
 //               one 16-bit product, and K needs no widening.
-//   P           fp16, exp2(s + log2 s_V - m + 2): the V scale enters through the exponent and
-//               leaves the sum in fp32; written over S in tensor memory, from where the second
-//               product takes it.
-//   O += P V    kind::f16. Four warps widen V blocks to fp16 (exact) in the 128-byte swizzled
-//               K-major layout; both query tiles use each widened block.
-// The row's reference m moves (and O in tensor memory is rescaled) only when a block's maximum
-// passes it by more than 2^13: fp16 then holds P from 2^15 down to steps of 2^-26 of the
-// reference, so that n keys behind a far larger one lose at most n 2^-27 of the sum.
+//   P           bf16, exp2(s + log2 s_V - m): the V scale enters through the exponent and leaves
+//               the sum in fp32; off by at most 2^-9 of itself; written over S in tensor memory,
+//               from where the second product takes it.
+//   O += P V    kind::f16 on bf16. Four warps widen V blocks to bf16 (exact) in the 128-byte
+//               swizzled K-major layout; both query tiles use each widened block.
+// bf16 has fp32's exponents, so the row's reference m is the maximum of its first block and stays
+// unless a block passes it by more than 2^64 (then O in tensor memory is rescaled): the weights
+// are taken against it while the block's maximum is found only to see that. With fp16 weights,
+// whose reference may lag by 2^13 at most, one step in five rescaled O on keys of unlike norms.
 //
 // The tensor pipe and the softmax of a lane depend on each other, so there are two lanes with
 // two S buffers of 64 keys each: a buffer's next scores are issued when the output of its last
@@ -28,8 +29,8 @@
 //     output of its own; the two outputs are joined at the end.
 //   head_dim 256: lane i takes every second block; one output (256 columns), for which the row's
 //     reference maximum goes from block to block between the two groups.
-// Warps: 0 loads of K, 2 loads of V, 1 scores, 3 outputs, 4..7 and 8..11 softmax of lane 0 and 1 (one thread
-// a row), 12..15 widening of V.
+// Warps: 0 and 1 scores, 2 and 3 outputs of lane 0 and 1, 4..7 and 8..11 softmax of lane 0 and 1
+// (one thread a row), 12..15 widening of V, 16 loads of K, 17 loads of V.
 #include <float.h>
 
 #include "kernels.h"
@@ -40,10 +41,10 @@ namespace vla {
 
 namespace {
 
-constexpr int kThreads = 512;
-// Registers: 128 a thread at launch; the softmax groups go up to 200, the two others down to
-// 56 (2 x 128 x 200 + 2 x 128 x 56 = 65536 = 512 x 128).
-constexpr float kLag = 13.0f, kLift = 2.0f;   // see m below
+constexpr int kThreads = 640;
+// Registers: 96 a thread at launch; the softmax groups go up to 168, the three others down to
+// 48 (2 x 128 x 168 + 3 x 128 x 48 = 61440 = 640 x 96).
+constexpr float kLag = 64.0f;
 
 template <int D>
 struct Tc {
@@ -79,7 +80,7 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 // The same value in every lane, as one the compiler knows to be uniform.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
-// E4M3 x E4M3 (kind::f8f6f4) and fp16 x fp16 (kind::f16): format fields 0, fp32 accumulator.
+// E4M3 x E4M3 (kind::f8f6f4): format fields 0, fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_fmt0(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
@@ -129,6 +130,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Two E4M3 bytes, each in the upper byte of a half word, to bf16: exponent and mantissa move to
+// bf16's places (a value 2^-120 of the right one, E4M3's subnormals among bf16's), times 2^120.
+__device__ __forceinline__ uint32_t e4m3_to_bf2(uint32_t v) {
+  const uint32_t u = ((v >> 4) & 0x07f007f0u) | (v & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x7b807b80u));
+  return r;
+}
 // 32 columns of this warp's 32 lanes; the caller waits (tmem_wait_ld).
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -160,23 +169,6 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {   // 
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
-}
-
-// Bounded wait for a phase in few instructions: each try suspends the thread for up to a
-// millisecond, 2000 of them give up. (Five roles run on an SM at once, and short loops are what
-// its instruction caches need.)
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int* err) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
-      "TRY:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t@p bra DONE;\n\t"
-      "add.u32 n, n, 1;\n\tsetp.lt.u32 p, n, 2000;\n\t@p bra TRY;\n\tsetp.ne.u32 p, 0, 0;\n\t"
-      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  if (__builtin_expect(!ok, 0)) report(err, kDevTimeout);
-  return ok != 0;
 }
 
 // How the lanes share a segment. Step k of lane i works in S buffer 2 i + (k & 1); scores and
@@ -222,13 +214,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::nk; ++i) {
       mbar_init(kfull + 8 * i, 1);
-      mbar_init(kempty + 8 * i, 1);
+      mbar_init(kempty + 8 * i, 2);
     }
     for (int i = 0; i < S::nv; ++i) {
       mbar_init(rfull + 8 * i, 1);
       mbar_init(rempty + 8 * i, 4);
       mbar_init(vfull + 8 * i, 4);
-      mbar_init(vempty + 8 * i, 1);
+      mbar_init(vempty + 8 * i, S::two ? 2 : 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(sfull + 8 * i, 1);
@@ -239,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     pdl_trigger();
   }
-  if (warp == 1) {
+  if (warp == 18) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (blockIdx.x == 0 && warp == 2)
+  if (blockIdx.x == 0 && warp == 19)
     for (int b = lane; b < p.batch; b += 32)
       if (kv8_tile(p, b, 0).slot < 0) report(p.err, kKv8BadRow);
   Kv8Walk w = kv8_walk(p);
@@ -255,13 +247,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   Kv8Segment g;
   bool ok = true;
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if ((warp == 0 || warp == 2) && lane == 0) {
-      // ---- loads: warp 0 the K blocks, warp 2 the V blocks
-      const uint8_t* src = warp == 0 ? p.c.k : p.c.v;
-      const uint32_t full = warp == 0 ? kfull : rfull, empty = warp == 0 ? kempty : rempty;
-      const uint32_t dst = sm + (warp == 0 ? S::k : S::v8);
-      const int ring = warp == 0 ? S::nk : S::nv;
+    // ---- products, each by a converged warp: warps 0 and 1 the scores of lane 0 and 1, warps 2
+    // and 3 the outputs (head_dim 256: warp 2 both lanes', in turn, as they share an output)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    const uint32_t lead = elect_one();
+    // the warp stays together when a wait gives up
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err)) != 0;
+    };
+    const uint32_t tm = uniform(tmem);
+    uint32_t ph = 0, rph = 0;                             // rph, rs: the ring of K or V
+    int rs = 0;
+    if (warp < 2) {
+      constexpr uint32_t id_s = idesc_fmt0(128, 64);
+      constexpr uint32_t kTile = (2 * S::q_half) >> 4;    // from one query tile to the next
+      const int i = warp;
+      const uint32_t q0 = uniform(desc_lo(sm + S::q)), k0 = uniform(desc_lo(sm + S::k));
+      uint32_t qph = 0;
+      while (ok && kv8_next(p, w, g)) {
+        const Plan pl = make_plan<D>(p, g);
+        wait_all(qfull, qph);
+        qph ^= 1;
+        const uint32_t a0 = uniform(q0 + (pl.tiles && i ? kTile : 0));
+        // every block in turn, also those of the other lane: a warp that skipped one could take its
+        // slot's last phase for the next
+        for (int j = 0; j < g.n && ok; ++j) {
+          wait_all(kfull + 8 * rs, rph);
+          if (pl.tiles || (j & 1) == i) {
+            const int k = pl.tiles ? j : j >> 1, buf = 2 * i + (k & 1);
+            // the buffer's last weights have been used
+            if (k >= 2) wait_all(odone + 8 * buf, buf_parity(ph, i, k - 2));
+            tc_fence_after();
+            if (!ok) break;
+            const uint32_t b0 = k0 + rs * (D * 64 >> 4);
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                umma_f8(lead, tm + buf * 64, a0 + ((term * S::q_half + (kk >> 1) * 8192) >> 4) + 2 * (kk & 1),
+                        b0 + (((kk >> 1) * 4096) >> 4) + 2 * (kk & 1), id_s, (term | kk) != 0 ? 1u : 0u);
+            umma_commit_if(lead, sfull + 8 * buf);
+            umma_commit_if(lead, kempty + 8 * rs);
+          } else if (lead) {
+            mbar_arrive(kempty + 8 * rs);
+          }
+          if (++rs == S::nk) {
+            rs = 0;
+            rph ^= 1;
+          }
+        }
+        ph = next_phases(ph, pl);
+      }
+    } else if (S::two || warp == 2) {
+      constexpr uint32_t id_o = idesc_bf16_f32(128, D);
+      const uint32_t v0 = uniform(desc_lo(sm + S::v16));
+      while (ok && kv8_next(p, w, g)) {
+        const Plan pl = make_plan<D>(p, g);
+        for (int j = 0; j < g.n && ok; ++j) {
+          wait_all(vfull + 8 * rs, rph);
+          const int i = S::two ? warp - 2 : j & 1;
+          if (pl.tiles || (j & 1) == i) {
+            const int k = pl.tiles ? j : j >> 1, buf = 2 * i + (k & 1);
+            wait_all(pfull + 8 * buf, buf_parity(ph, i, k));
+            tc_fence_after();
+            if (!ok) break;
+            const uint32_t acc = (S::two ? k : j) == 0 ? 0u : 1u, b0 = v0 + rs * (D * 128 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts(lead, tm + S::o_col + (S::two ? i * D : 0), tm + buf * 64 + kk * 8, b0 + 2 * kk, id_o,
+                          kk == 0 ? acc : 1u);
+            // (no commit follows the last output's own, for which the CTA waits before it ends)
+            umma_commit_if(lead, vempty + 8 * rs);
+            umma_commit_if(lead, odone + 8 * buf);
+          } else if (lead) {
+            mbar_arrive(vempty + 8 * rs);
+          }
+          if (++rs == S::nv) {
+            rs = 0;
+            rph ^= 1;
+          }
+        }
+        ph = next_phases(ph, pl);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp < 18 && lane == 0) {
+      // ---- loads: warp 16 the K blocks, warp 17 the V blocks
+      const uint8_t* src = warp == 16 ? p.c.k : p.c.v;
+      const uint32_t full = warp == 16 ? kfull : rfull, empty = warp == 16 ? kempty : rempty;
+      const uint32_t dst = sm + (warp == 16 ? S::k : S::v8);
+      const int ring = warp == 16 ? S::nk : S::nv;
       int n = 0, s = 0;
       uint32_t ph = 1;
       while (ok && kv8_next(p, w, g)) {
@@ -282,92 +359,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // no copies left in flight
       for (int i = n > ring ? n - ring : 0; i < n; ++i) mbar_wait(full + 8 * (i % ring), (i / ring) & 1, p.err);
-    } else if (warp == 1 || warp == 3) {
-      // ---- products, each by a converged warp: warp 1 the scores, warp 3 the outputs
-      const uint32_t lead = elect_one();
-      // the warp stays together when a wait gives up
-      auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && wait_for(bar, parity, p.err)) != 0;
-      };
-      const uint32_t tm = uniform(tmem);
-      uint32_t ph = 0, qph = 0, rph = 0;                  // rph, rs: the ring of K or V
-      int rs = 0;
-      if (warp == 1) {
-        constexpr uint32_t id_s = idesc_fmt0(128, 64);
-        constexpr uint32_t kTile = (2 * S::q_half) >> 4;  // from one query tile to the next
-        const uint32_t q0 = uniform(desc_lo(sm + S::q)), k0 = uniform(desc_lo(sm + S::k));
-        while (ok && kv8_next(p, w, g)) {
-          const Plan pl = make_plan<D>(p, g);
-          const int steps = pl.steps[0] + pl.steps[1];
-          wait_all(qfull, qph);
-          qph ^= 1;
-          for (int t = 0; t < steps && ok; ++t) {
-            const int i = t & 1, k = t >> 1, buf = 2 * i + (k & 1);
-            if (!pl.tiles || i == 0) wait_all(kfull + 8 * rs, rph);
-            // the buffer's last weights have been used
-            if (k >= 2) wait_all(odone + 8 * buf, buf_parity(ph, i, k - 2));
-            tc_fence_after();
-            if (!ok) break;
-            const uint32_t a0 = q0 + (pl.tiles && i ? kTile : 0), b0 = k0 + rs * (D * 64 >> 4);
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                umma_f8(lead, tm + buf * 64, a0 + ((term * S::q_half + (kk >> 1) * 8192) >> 4) + 2 * (kk & 1),
-                        b0 + (((kk >> 1) * 4096) >> 4) + 2 * (kk & 1), id_s, (term | kk) != 0 ? 1u : 0u);
-            if (!pl.tiles || i == 1) {
-              umma_commit_if(lead, kempty + 8 * rs);
-              if (++rs == S::nk) {
-                rs = 0;
-                rph ^= 1;
-              }
-            }
-            umma_commit_if(lead, sfull + 8 * buf);
-          }
-          ph = next_phases(ph, pl);
-        }
-      } else {
-        constexpr uint32_t id_o = idesc_fmt0(128, D);
-        const uint32_t v0 = uniform(desc_lo(sm + S::v16));
-        while (ok && kv8_next(p, w, g)) {
-          const Plan pl = make_plan<D>(p, g);
-          const int steps = pl.steps[0] + pl.steps[1];
-          for (int t = 0; t < steps && ok; ++t) {
-            const int i = t & 1, k = t >> 1, buf = 2 * i + (k & 1);
-            if (!pl.tiles || i == 0) wait_all(vfull + 8 * rs, rph);
-            wait_all(pfull + 8 * buf, buf_parity(ph, i, k));
-            tc_fence_after();
-            if (!ok) break;
-            const uint32_t acc = (S::two ? k : t) == 0 ? 0u : 1u, b0 = v0 + rs * (D * 128 >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ts(lead, tm + S::o_col + (S::two ? i * D : 0), tm + buf * 64 + kk * 8, b0 + 2 * kk, id_o,
-                          kk == 0 ? acc : 1u);
-            if (!pl.tiles || i == 1) {
-              umma_commit_if(lead, vempty + 8 * rs);
-              if (++rs == S::nv) {
-                rs = 0;
-                rph ^= 1;
-              }
-            }
-            // (no commit follows the last output's own, for which the CTA waits before it ends)
-            umma_commit_if(lead, odone + 8 * buf);
-          }
-          ph = next_phases(ph, pl);
-        }
-      }
     }
     __syncwarp();
   } else if (warp >= 12) {
-    // ---- V blocks to fp16: [D rows][64 positions] bytes, 64-byte swizzle, to halves, 128-byte
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ---- V blocks to bf16: [D rows][64 positions] bytes, 64-byte swizzle, to 128-byte rows
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     const int tid = threadIdx.x - 384;
     int vt = 0;
     while (kv8_next(p, w, g)) {
       for (int j = 0; j < g.n; ++j, ++vt) {
         const int r = vt % S::nv;
-        ok = ok && wait_for(rfull + 8 * r, (vt / S::nv) & 1, p.err);
-        ok = ok && (vt < S::nv || wait_for(vempty + 8 * r, (vt / S::nv - 1) & 1, p.err));
+        ok = ok && mbar_wait(rfull + 8 * r, (vt / S::nv) & 1, p.err);
+        ok = ok && (vt < S::nv || mbar_wait(vempty + 8 * r, (vt / S::nv - 1) & 1, p.err));
         if (ok) {
           const uint8_t* src = smem + S::v8 + r * D * 64;
           uint8_t* dst = smem + S::v16 + r * D * 128;
@@ -376,14 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int d = i >> 2, c = i & 3;
             const uint4 x = *reinterpret_cast<const uint4*>(src + d * 64 + ((c ^ ((d >> 1) & 3)) << 4));
             uint4 y, z;
-            y.x = e4m3x2_to_h2(static_cast<uint16_t>(x.x));
-            y.y = e4m3x2_to_h2(static_cast<uint16_t>(x.x >> 16));
-            y.z = e4m3x2_to_h2(static_cast<uint16_t>(x.y));
-            y.w = e4m3x2_to_h2(static_cast<uint16_t>(x.y >> 16));
-            z.x = e4m3x2_to_h2(static_cast<uint16_t>(x.z));
-            z.y = e4m3x2_to_h2(static_cast<uint16_t>(x.z >> 16));
-            z.z = e4m3x2_to_h2(static_cast<uint16_t>(x.w));
-            z.w = e4m3x2_to_h2(static_cast<uint16_t>(x.w >> 16));
+            y.x = e4m3_to_bf2(__byte_perm(x.x, 0, 0x1404));
+            y.y = e4m3_to_bf2(__byte_perm(x.x, 0, 0x3424));
+            y.z = e4m3_to_bf2(__byte_perm(x.y, 0, 0x1404));
+            y.w = e4m3_to_bf2(__byte_perm(x.y, 0, 0x3424));
+            z.x = e4m3_to_bf2(__byte_perm(x.z, 0, 0x1404));
+            z.y = e4m3_to_bf2(__byte_perm(x.z, 0, 0x3424));
+            z.z = e4m3_to_bf2(__byte_perm(x.w, 0, 0x1404));
+            z.w = e4m3_to_bf2(__byte_perm(x.w, 0, 0x3424));
             *reinterpret_cast<uint4*>(dst + d * 128 + (((2 * c) ^ (d & 7)) << 4)) = y;
             *reinterpret_cast<uint4*>(dst + d * 128 + (((2 * c + 1) ^ (d & 7)) << 4)) = z;
           }
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int grp = (warp - 4) >> 2, qd = warp & 3, r = qd * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(qd * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + S::xch);
@@ -487,12 +490,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scale_of = [&](int k) { return __ldg(scales + min(first + k * stride, g.n - 1)); };
       float4 sc = scale_of(0);
       float m = -INFINITY, l = 0.0f;
-      auto load = [&](int k, float (&x)[64]) {            // the scores of step k, in flight
-        ok = ok && wait_for(sfull + 8 * (2 * grp + (k & 1)), buf_parity(ph, grp, k), p.err);
+      // the scores of step k, in flight: half h of the block's keys to x + 32 h
+      auto load_half = [&](int k, int h, float* x) {
+        tmem_ld32_async(tl + (2 * grp + (k & 1)) * 64 + 32 * h, x);
+      };
+      auto wait_scores = [&](int k) {
+        ok = ok && mbar_wait(sfull + 8 * (2 * grp + (k & 1)), buf_parity(ph, grp, k), p.err);
         tc_fence_after();
-        const uint32_t ts = tl + (2 * grp + (k & 1)) * 64;
-        tmem_ld32_async(ts, x);
-        tmem_ld32_async(ts + 32, x + 32);
+      };
+      auto scores_there = [&](int k) {
+        if (k >= steps) return false;
+        const bool there = __all_sync(0xffffffffu, mbar_try_wait(sfull + 8 * (2 * grp + (k & 1)), buf_parity(ph, grp, k))) != 0;
+        tc_fence_after();
+        return there;
       };
       // moves the row's reference to nm, and with it l and (if it has begun) this warp's rows of O:
       // after the last product on them
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         const int before = S::two ? k - 1 : (j - 1) >> 1, of = S::two ? grp : grp ^ 1;
         if ((S::two ? k : j) > 0) {
-          ok = ok && wait_for(odone + 8 * (2 * of + (before & 1)), buf_parity(ph, of, before), p.err);
+          ok = ok && mbar_wait(odone + 8 * (2 * of + (before & 1)), buf_parity(ph, of, before), p.err);
           tc_fence_after();
           const uint32_t to = tl + S::o_col + (S::two ? grp * D : 0);
 #pragma unroll 1
@@ -518,75 +528,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       float x[64];
-      if (steps > 0) load(0, x);
+      bool loaded = false;                                // the step's scores are in flight
       for (int k = 0; k < steps; ++k) {
         const int buf = 2 * grp + (k & 1), j = first + k * stride, key0 = (g.blk + j) * kKv8Block;
+        if (!loaded) {
+          wait_scores(k);
+          load_half(k, 0, x);
+          load_half(k, 1, x + 32);
+        }
         const float gk = fmaxf(rowf * sc.x, FLT_MIN);       // (never 0: a masked score stays -infinity)
         const int ev = exp_of(sc.y);
         const float fv = static_cast<float>(ev), un = exp2i(-ev);
         sc = scale_of(k + 1);
         tmem_wait_ld();
+        auto settle = [&]() {                             // x is not used before the wait; masked scores
 #pragma unroll
-        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(x[c]));   // not used before the wait
-        if (__builtin_expect(key0 < lo_last || key0 + 64 > hi_first, 0)) {
+          for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(x[c]));
+          if (__builtin_expect(key0 < lo_last || key0 + 64 > hi_first, 0)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c < lo - key0 || c >= hi - key0) x[c] = -INFINITY;
-        }
-        // the block's largest score. (-infinity times gk stays -infinity: gk > 0)
-        auto largest = [&]() {
+            for (int c = 0; c < 64; ++c)
+              if (c < lo - key0 || c >= hi - key0) x[c] = -INFINITY;
+          }
+        };
+        settle();
+        // the largest of half of the block's scores
+        auto largest = [&](const float* x) {
           float h[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 4; c < 60; c += 8)
+          for (int c = 4; c < 28; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = max3(h[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[60 + i]);
-          return fmaf(max3(h[0], h[1], fmaxf(h[2], h[3])), gk, fv);
+          for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[28 + i]);
+          return max3(h[0], h[1], fmaxf(h[2], h[3]));
         };
         auto passes = [&](float mx) { return mx > m + kLag || (m == -INFINITY && mx > m); };
-        if (!S::two) {
-          // the reference of the block before comes from the other group, this block's goes to it
-          const float mx = largest();
-          if (j > 0) {
+        if (!S::two || k == 0) {
+          // (-infinity times gk stays -infinity: gk > 0)
+          const float mx = fmaf(fmaxf(largest(x), largest(x + 32)), gk, fv);
+          if (!S::two && j > 0) {
+            // head_dim 256: the reference of the block before comes from the other group, this
+            // block's goes to it
             named_bar_sync(1 + (grp ^ 1) * 4 + qd, 64);
             const float old = xch[((j - 1) & 1) * 128 + r];
             if (old != m) l *= exp2_approx(m - old);      // (m = -infinity: l is 0)
             m = old;
           }
           const bool move = passes(mx);
-          if (j + 1 < g.n) {
+          if (!S::two && j + 1 < g.n) {
             xch[(j & 1) * 128 + r] = move ? mx : m;
             asm volatile("bar.arrive %0, 64;" ::"r"(1 + grp * 4 + qd) : "memory");
           }
-          if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) move_to(move ? mx : m, k, j);
+          if (__any_sync(0xffffffffu, move)) move_to(move ? mx : m, k, j);
         }
         uint32_t pk[32];                                  // positions 2 i, 2 i + 1 of the block
         float sum;
         while (true) {
-          const float off = fv + (m == -INFINITY ? 0.0f : kLift - m);
+          const float off = fv - (m == -INFINITY ? 0.0f : m);
           float2 s2 = make_float2(0.0f, 0.0f);
+          float raw = -INFINITY;
+          loaded = scores_there(k + 1);
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(gk, gk), make_float2(off, off));
-            const float2 w2 = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-            s2 = add2(s2, w2);
-            const __half2 h2 = __floats2half2_rn(w2.x, w2.y);
-            // tokens 16 w + 8 h + 2 t, + 1 stand at positions 16 t + 4 w + 2 h, + 1
-            pk[((c >> 1) & 3) * 8 + (c >> 4) * 2 + ((c >> 3) & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+          for (int hf = 0; hf < 2; ++hf) {
+            if (S::two) raw = fmaxf(raw, largest(x + 32 * hf));
+#pragma unroll
+            for (int c = 32 * hf; c < 32 * hf + 32; c += 2) {
+              const float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(gk, gk), make_float2(off, off));
+              const float2 w2 = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+              s2 = add2(s2, w2);
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(w2.x, w2.y);
+              // tokens 16 w + 8 h + 2 t, + 1 stand at positions 16 t + 4 w + 2 h, + 1
+              pk[((c >> 1) & 3) * 8 + (c >> 4) * 2 + ((c >> 3) & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            if (loaded) load_half(k + 1, hf, x + 32 * hf);
           }
           sum = s2.x + s2.y;
           if (!S::two) break;
-          // head_dim <= 128: the weights against the reference as it stood, the maximum found
-          // meanwhile; once more if it passes the reference too far (rare after the first block)
-          const float mx = largest();
+          // head_dim <= 128: the weights were taken against the reference as it stood; if the
+          // block's maximum passes it too far, once more with the scores read again
+          const float mx = fmaf(raw, gk, fv);
           const bool move = passes(mx);
           if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
           move_to(move ? mx : m, k, j);
+          load_half(k, 0, x);
+          load_half(k, 1, x + 32);
+          tmem_wait_ld();
+          settle();
         }
         l = fmaf(sum, un, l);
         tmem_st32_async(tl + buf * 64, pk);
-        if (k + 1 < steps) load(k + 1, x);                // (in flight while the weights are stored)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -623,14 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last products on the outputs read here. A wait may look one phase ahead only, so the
         // groups of head_dim 256 wait for the last two blocks in order.
         if (S::two) {
-          ok = ok && wait_for(odone + 8 * (2 * grp + ((steps - 1) & 1)), buf_parity(ph, grp, steps - 1), p.err);
+          ok = ok && mbar_wait(odone + 8 * (2 * grp + ((steps - 1) & 1)), buf_parity(ph, grp, steps - 1), p.err);
           if (join && pl.steps[1] > 0) {
             const int e = pl.steps[1] - 1;
-            ok = ok && wait_for(odone + 8 * (2 + (e & 1)), buf_parity(ph, 1, e), p.err);
+            ok = ok && mbar_wait(odone + 8 * (2 + (e & 1)), buf_parity(ph, 1, e), p.err);
           }
         } else {
           for (int t = max(0, g.n - 2); t < g.n; ++t)
-            ok = ok && wait_for(odone + 8 * (2 * (t & 1) + ((t >> 1) & 1)), buf_parity(ph, t & 1, t >> 1), p.err);
+            ok = ok && mbar_wait(odone + 8 * (2 * (t & 1) + ((t >> 1) & 1)), buf_parity(ph, t & 1, t >> 1), p.err);
         }
         tc_fence_after();
         const bool have1 = join && pl.steps[1] > 0;
@@ -677,10 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (row_ok && (S::two || grp == 0)) {
-          if (!g.whole) p.ws_ml[slot * S::rows + tr] = make_float2(m - kLift, l);
+          if (!g.whole) p.ws_ml[slot * S::rows + tr] = make_float2(m, l);
           else if (p.lse)
             p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] =
-                l == 0.0f ? -INFINITY : (m - kLift + log2f(l)) * 0.6931471805599453f;
+                l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
         tc_fence_before();
       }
@@ -693,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 18) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
