@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
         for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * R + 8 * n + 2 * t + c].x);
         fac[n][c] = m[n][c] == -INFINITY ? 1.0f : exp2_approx(m[n][c] - mm);
       }
-    const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
+    const int slot = g.slot;
     float* xb = reinterpret_cast<float*>(smem + S::xch);
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += S::cols) {
@@ -417,10 +417,10 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
 
 // ---- merging the parts of the items that more than one CTA worked on
 
-// The item that the cut before part `cut` lies in, if it is the first cut inside that item.
+// The item that the cut before part `cut` lies in, if it is the first cut that stays inside that item.
 struct Kv8Cut {
   int b, tile, head, rows;      // rows: query rows of the tile
-  int u0, c0, c1;               // the item's first unit; parts c0 .. c1 - 1 meet it
+  int c0, c1;                   // parts c0 .. c1 - 1 meet the item
 };
 __device__ __forceinline__ bool kv8_cut(const Kv8AttendParams& p, const Kv8Line& line, int cut, Kv8Cut& r) {
   const int uc = kv8_begin(line, cut);
@@ -428,9 +428,9 @@ __device__ __forceinline__ bool kv8_cut(const Kv8AttendParams& p, const Kv8Line&
   int inside;
   const int e = kv8_find(p, line, uc, &inside);
   const Kv8Tile row = kv8_tile(p, p.by_tiles.div(e), p.by_tiles.mod(e));
-  r.u0 = uc - inside % row.units;
-  if (uc == r.u0 || kv8_begin(line, cut - 1) > r.u0) return false;
-  const int u1 = r.u0 + row.units;
+  // cuts of [u0 + snap + 1, u1 - snap - 1] stay
+  const int u0 = uc - inside % row.units + line.snap, u1 = u0 + row.units - 2 * line.snap;
+  if (uc <= u0 || uc >= u1 || kv8_begin(line, cut - 1) > u0) return false;
   r.b = p.by_tiles.div(e);
   r.tile = e - r.b * p.tiles;
   r.head = inside / row.units;
@@ -440,11 +440,6 @@ __device__ __forceinline__ bool kv8_cut(const Kv8AttendParams& p, const Kv8Line&
   r.c1 = min(p.grid, cut + (line.per > 0 ? (u1 - uc - 1) / line.per + 1 : u1 - uc));
   while (r.c1 > cut && kv8_begin(line, r.c1 - 1) >= u1) --r.c1;
   return true;
-}
-// Place of a part in the workspace: the item in which a CTA's range starts is its first, one
-// that starts later its second.
-__device__ __forceinline__ int kv8_slot(const Kv8Line& line, const Kv8Cut& r, int c) {
-  return 2 * c + (kv8_begin(line, c) >= r.u0 ? 0 : 1);
 }
 
 constexpr int kMergeWarps = 8;
@@ -473,7 +468,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_rows_kernel(const 
     float2 ml = make_float2(-INFINITY, 0.0f);
     int at = 0;
     if (c < cut.c1) {
-      at = kv8_slot(line, cut, c) * p.tile_rows + r;
+      at = kv8_slot(c, c == cut.c0) * p.tile_rows + r;
       ml = p.ws_ml[at];
     }
     float nm = ml.x;
@@ -555,10 +550,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_tiles_kernel(const
   pdl_wait();
   if (!mine || r >= cut.rows) return;
   float mm = -INFINITY, ll = 0.0f;
-  for (int c = cut.c0; c < cut.c1; ++c) mm = fmaxf(mm, p.ws_ml[kv8_slot(line, cut, c) * p.tile_rows + r].x);
+  for (int c = cut.c0; c < cut.c1; ++c) mm = fmaxf(mm, p.ws_ml[kv8_slot(c, c == cut.c0) * p.tile_rows + r].x);
   float4 v[kG] = {};
   for (int c = cut.c0; c < cut.c1; ++c) {
-    const int slot = kv8_slot(line, cut, c);
+    const int slot = kv8_slot(c, c == cut.c0);
     const float2 ml = p.ws_ml[slot * p.tile_rows + r];
     const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - mm);
     ll = fmaf(ml.y, f, ll);

@@ -2,7 +2,7 @@
 // a prompt piece), on the tcgen05 tensor cores.
 //
 // Same formula and the same equal division of the work as kv8_attend.cu, in tiles of 128
-// query rows (head_dim 256) or 256 (smaller head_dim) and units of 128 keys. What bounds it
+// query rows (head_dim 256) or 256 (smaller head_dim) and units of 64 keys. What bounds it
 // is the tensor pipe and, at head_dim 64 and 128, the exponentials (16 a clock and SM).
 //
 //   S = Q K^T   kind::f8f6f4, K as the cache holds it (its block is already the operand's
@@ -16,10 +16,11 @@
 //               from where the second product takes it.
 //   O += P V    kind::f16 on bf16. Four warps widen V blocks to bf16 (exact) in the 128-byte
 //               swizzled K-major layout; both query tiles use each widened block.
-// bf16 has fp32's exponents, so the row's reference m is the maximum of its first block and stays
-// unless a block passes it by more than 2^64 (then O in tensor memory is rescaled): the weights
-// are taken against it while the block's maximum is found only to see that. With fp16 weights,
-// whose reference may lag by 2^13 at most, one step in five rescaled O on keys of unlike norms.
+// bf16 has fp32's exponents, so the row's reference m is the maximum of the first block it sees
+// and stays unless a block passes it by far (then O in tensor memory is rescaled). At head_dim 64
+// and 128 no other maximum is looked for: the weights' sum shows whether they were too large, and
+// then the block is done once more. With fp16 weights, whose reference may lag by 2^13 at most,
+// one step in five rescaled O on keys of unlike norms.
 //
 // The tensor pipe and the softmax of a lane depend on each other, so there are two lanes with
 // two S buffers of 64 keys each: a buffer's next scores are issued when the output of its last
@@ -44,7 +45,11 @@ namespace {
 constexpr int kThreads = 640;
 // Registers: 96 a thread at launch; the softmax groups go up to 168, the three others down to
 // 48 (2 x 128 x 168 + 3 x 128 x 48 = 61440 = 640 x 96).
-constexpr float kLag = 64.0f;
+
+// The reference moves when a block's largest exponent is above it by more than kLag (head_dim
+// 256), its weights sum to more than kMaxSum (else). A row's sum of exponentials leaves the V
+// scale (>= 2^-60) out of its terms: 2^40 or 64 times 2^32, times 2^60, times 2^20 blocks stay below 2^127.
+constexpr float kLag = 32.0f, kMaxSum = 1099511627776.0f;
 
 template <int D>
 struct Tc {
@@ -138,6 +143,8 @@ __device__ __forceinline__ uint32_t e4m3_to_bf2(uint32_t v) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x7b807b80u));
   return r;
 }
+// Exponent that Q's row of largest magnitude `am` is divided by.
+__device__ __forceinline__ int q_exp(float am) { return am > 0.0f ? min(max(exp_of(am) - 7, -118), 120) : 0; }
 // 32 columns of this warp's 32 lanes; the caller waits (tmem_wait_ld).
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -411,53 +418,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r0 = g.tile * S::rows + (pl.tiles ? grp * 128 : 0); // first row of this group's tile
       const int row = r0 + r, rows = min(128, left - (pl.tiles ? grp * 128 : 0));
       const bool row_ok = r < rows;
-      // ---- Q to E4M3 pairs: this thread's row (head_dim 256: half of it)
+      // ---- Q to E4M3 pairs: a load brings whole rows (D / 8 lanes each) of the warp's 32
+      // (head_dim 256: of its half of them), and every lane keeps its own row's factor
       float rowf = p.scale_log2;
       {
-        constexpr int kQ = S::two ? D : D / 2;
-        const int d0 = S::two ? 0 : grp * kQ;
-        const bool load = S::two ? (pl.tiles || grp == 0) : true;
-        const __nv_bfloat16* q = p.q + g.b * p.q_st[0] + p.by_group.div(row) * p.q_st[1] +
-                                 (g.head * p.group + p.by_group.mod(row)) * p.q_st[2] + d0;
-        // the largest magnitude (a second group on the same rows needs it for the row's factor)
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kLoads = (S::two ? 32 : 16) / kAt;
+        const int half = S::two ? 0 : grp * 16, d = lane % kLanes * 8;
+        const long long at = g.b * p.q_st[0] + p.by_group.div(row) * p.q_st[1] +
+                             (g.head * p.group + p.by_group.mod(row)) * p.q_st[2];
+        uint8_t* dst = smem + S::q + (pl.tiles ? grp * 2 * S::q_half : 0) + (d >> 6) * 8192 + (d & 8);
         float am = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < kQ / 8; ++i) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (row_ok && d0 + i * 8 < p.c.D) x = *reinterpret_cast<const uint4*>(q + i * 8);
-          const uint32_t v[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
+#pragma unroll 1
+        for (int i0 = 0; i0 < kLoads; i0 += 8) {
+          uint4 x[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {                   // bf16 bits order like their values; not finite: left out
-            const uint32_t a = v[c] & 0xffffu, b = v[c] >> 16;
-            am = fmaxf(am, __uint_as_float(a < 0x7f80u ? a << 16 : 0u));
-            am = fmaxf(am, __uint_as_float(b < 0x7f80u ? b << 16 : 0u));
+          for (int i = 0; i < 8; ++i) {
+            const int rr = half + (i0 + i) * kAt + lane / kLanes;
+            const long long from = __shfl_sync(0xffffffffu, at, rr);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (qd * 32 + rr < rows && d < p.c.D) x[i] = *reinterpret_cast<const uint4*>(p.q + from + d);
           }
-        }
-        if (!S::two) {                                    // over both halves of the row
-          xch[grp * 128 + r] = am;
-          named_bar_sync(11 + qd, 64);
-          am = fmaxf(am, xch[(grp ^ 1) * 128 + r]);
-          named_bar_sync(11 + qd, 64);
-        }
-        const int e = am > 0.0f ? min(max(exp_of(am) - 7, -118), 120) : 0;
-        const float inv = exp2i(-e);
-        rowf *= exp2i(e);
-        if (load) {
-          uint8_t* dst = smem + S::q + (pl.tiles ? grp * 2 * S::q_half : 0) + r * 64;
-#pragma unroll 2
-          for (int i = 0; i < kQ / 16; ++i) {             // 16 dims: one 16-byte chunk of each term
-            uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if (row_ok && d0 + i * 16 < p.c.D) {
-              x[0] = *reinterpret_cast<const uint4*>(q + i * 16);
-              x[1] = *reinterpret_cast<const uint4*>(q + i * 16 + 8);
-            }
-            uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = half + (i0 + i) * kAt + lane / kLanes;
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            // the row's largest magnitude (bf16 bits order like their values; not finite: left out)
+            uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 y = x[c >> 1];
-              const uint32_t v0 = (c & 1) ? y.z : y.x, v1 = (c & 1) ? y.w : y.y;
-              float f[4] = {__uint_as_float(v0 << 16) * inv, __uint_as_float(v0 & 0xffff0000u) * inv,
-                            __uint_as_float(v1 << 16) * inv, __uint_as_float(v1 & 0xffff0000u) * inv};
+              const uint32_t a = v[c] & 0x7fffu, b = (v[c] >> 16) & 0x7fffu;
+              top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float big = __uint_as_float(top << 16);
+            const float inv = exp2i(-q_exp(big));
+            if (S::two) {
+              const float own = __shfl_sync(0xffffffffu, big, lane % kAt * kLanes);
+              if (lane / kAt == i0 + i) am = own;
+            } else if (lane == 0) {
+              xch[qd * 32 + rr] = big;
+            }
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float f[4] = {__uint_as_float(v[2 * c] << 16) * inv, __uint_as_float(v[2 * c] & 0xffff0000u) * inv,
+                            __uint_as_float(v[2 * c + 1] << 16) * inv, __uint_as_float(v[2 * c + 1] & 0xffff0000u) * inv};
 #pragma unroll
               for (int k = 0; k < 4; ++k) f[k] = fmaf(f[k], 0.0f, f[k]);   // an infinity becomes NaN
               const uint16_t h0 = f2_to_e4m3x2(f[0], f[1]), h1 = f2_to_e4m3x2(f[2], f[3]);
@@ -468,19 +474,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               lo[c] = f2_to_e4m3x2(f[0] - g0.x, f[1] - g0.y) |
                       (static_cast<uint32_t>(f2_to_e4m3x2(f[2] - g1.x, f[3] - g1.y)) << 16);
             }
-            const int d = d0 + i * 16;
-            uint8_t* a = dst + (d >> 6) * 8192 + ((((d >> 4) & 3) ^ ((r >> 1) & 3)) << 4);
-            *reinterpret_cast<uint4*>(a) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(a + S::q_half) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (!S::two || pl.tiles || grp == 0) {
+              const int t = qd * 32 + rr;
+              uint8_t* a = dst + t * 64 + ((((d >> 4) & 3) ^ ((t >> 1) & 3)) << 4);
+              *reinterpret_cast<uint2*>(a) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(a + S::q_half) = make_uint2(lo[0], lo[1]);
+            }
           }
         }
+        if (!S::two) {                                    // each group has read half of the rows
+          named_bar_sync(11 + qd, 64);
+          am = xch[r];
+          named_bar_sync(11 + qd, 64);
+        }
+        rowf *= exp2i(q_exp(am));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull);
       }
 
       int lo, hi, lo_last, hi_first, t0, t1;
-      kv8_seen(p, g.row, p.by_group.div(row), lo, hi);
+      kv8_seen(p, g.row, p.by_group.div(r0 + max(min(r, rows - 1), 0)), lo, hi);
       kv8_seen(p, g.row, p.by_group.div(r0), t0, hi_first);
       kv8_seen(p, g.row, p.by_group.div(r0 + max(rows, 1) - 1), lo_last, t1);
       const float4* scales = p.c.scale +
@@ -490,20 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scale_of = [&](int k) { return __ldg(scales + min(first + k * stride, g.n - 1)); };
       float4 sc = scale_of(0);
       float m = -INFINITY, l = 0.0f;
-      // the scores of step k, in flight: half h of the block's keys to x + 32 h
-      auto load_half = [&](int k, int h, float* x) {
-        tmem_ld32_async(tl + (2 * grp + (k & 1)) * 64 + 32 * h, x);
-      };
-      auto wait_scores = [&](int k) {
-        ok = ok && mbar_wait(sfull + 8 * (2 * grp + (k & 1)), buf_parity(ph, grp, k), p.err);
-        tc_fence_after();
-      };
-      auto scores_there = [&](int k) {
-        if (k >= steps) return false;
-        const bool there = __all_sync(0xffffffffu, mbar_try_wait(sfull + 8 * (2 * grp + (k & 1)), buf_parity(ph, grp, k))) != 0;
-        tc_fence_after();
-        return there;
-      };
       // moves the row's reference to nm, and with it l and (if it has begun) this warp's rows of O:
       // after the last product on them
       auto move_to = [&](float nm, int k, int j) {
@@ -527,93 +527,83 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
         }
       };
-      float x[64];
-      bool loaded = false;                                // the step's scores are in flight
       for (int k = 0; k < steps; ++k) {
         const int buf = 2 * grp + (k & 1), j = first + k * stride, key0 = (g.blk + j) * kKv8Block;
-        if (!loaded) {
-          wait_scores(k);
-          load_half(k, 0, x);
-          load_half(k, 1, x + 32);
-        }
+        ok = ok && mbar_wait(sfull + 8 * buf, buf_parity(ph, grp, k), p.err);
+        tc_fence_after();
         const float gk = fmaxf(rowf * sc.x, FLT_MIN);       // (never 0: a masked score stays -infinity)
         const int ev = exp_of(sc.y);
         const float fv = static_cast<float>(ev), un = exp2i(-ev);
         sc = scale_of(k + 1);
-        tmem_wait_ld();
-        auto settle = [&]() {                             // x is not used before the wait; masked scores
+        float x[64];
+        auto load = [&] {
+          tmem_ld32_async(tl + buf * 64, x);
+          tmem_ld32_async(tl + buf * 64 + 32, x + 32);
+          tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(x[c]));
+          for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(x[c]));   // x is not used before the wait
           if (__builtin_expect(key0 < lo_last || key0 + 64 > hi_first, 0)) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c < lo - key0 || c >= hi - key0) x[c] = -INFINITY;
           }
         };
-        settle();
-        // the largest of half of the block's scores
-        auto largest = [&](const float* x) {
+        // the block's largest score (-infinity times gk stays -infinity: gk > 0)
+        auto largest = [&] {
           float h[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 4; c < 28; c += 8)
+          for (int c = 4; c < 60; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = max3(h[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[28 + i]);
-          return max3(h[0], h[1], fmaxf(h[2], h[3]));
+          for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[60 + i]);
+          return fmaf(max3(h[0], h[1], fmaxf(h[2], h[3])), gk, fv);
         };
-        auto passes = [&](float mx) { return mx > m + kLag || (m == -INFINITY && mx > m); };
-        if (!S::two || k == 0) {
-          // (-infinity times gk stays -infinity: gk > 0)
-          const float mx = fmaf(fmaxf(largest(x), largest(x + 32)), gk, fv);
-          if (!S::two && j > 0) {
-            // head_dim 256: the reference of the block before comes from the other group, this
-            // block's goes to it
+        load();
+        if (!S::two) {
+          // head_dim 256: the reference of the block before comes from the other group, this
+          // block's goes to it
+          const float mx = largest();
+          if (j > 0) {
             named_bar_sync(1 + (grp ^ 1) * 4 + qd, 64);
             const float old = xch[((j - 1) & 1) * 128 + r];
-            if (old != m) l *= exp2_approx(m - old);      // (m = -infinity: l is 0)
+            if (old != m) l *= exp2_approx(m - old);        // (m = -infinity: l is 0)
             m = old;
           }
-          const bool move = passes(mx);
-          if (!S::two && j + 1 < g.n) {
+          const bool move = mx > m + kLag || (m == -INFINITY && mx > m);
+          if (j + 1 < g.n) {
             xch[(j & 1) * 128 + r] = move ? mx : m;
             asm volatile("bar.arrive %0, 64;" ::"r"(1 + grp * 4 + qd) : "memory");
           }
           if (__any_sync(0xffffffffu, move)) move_to(move ? mx : m, k, j);
         }
-        uint32_t pk[32];                                  // positions 2 i, 2 i + 1 of the block
+        uint32_t pk[32];                                    // positions 2 i, 2 i + 1 of the block
         float sum;
+        bool move = S::two && m == -INFINITY;
+        bool check = S::two;
         while (true) {
+          if (S::two && __any_sync(0xffffffffu, move)) {
+            const float mx = largest();
+            move_to(move ? fmaxf(m, mx) : m, k, j);
+          }
           const float off = fv - (m == -INFINITY ? 0.0f : m);
           float2 s2 = make_float2(0.0f, 0.0f);
-          float raw = -INFINITY;
-          loaded = scores_there(k + 1);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            if (S::two) raw = fmaxf(raw, largest(x + 32 * hf));
-#pragma unroll
-            for (int c = 32 * hf; c < 32 * hf + 32; c += 2) {
-              const float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(gk, gk), make_float2(off, off));
-              const float2 w2 = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-              s2 = add2(s2, w2);
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(w2.x, w2.y);
-              // tokens 16 w + 8 h + 2 t, + 1 stand at positions 16 t + 4 w + 2 h, + 1
-              pk[((c >> 1) & 3) * 8 + (c >> 4) * 2 + ((c >> 3) & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            if (loaded) load_half(k + 1, hf, x + 32 * hf);
+          for (int c = 0; c < 64; c += 2) {
+            const float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(gk, gk), make_float2(off, off));
+            const float2 w2 = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            s2 = add2(s2, w2);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(w2.x, w2.y);
+            // tokens 16 w + 8 h + 2 t, + 1 stand at positions 16 t + 4 w + 2 h, + 1
+            pk[((c >> 1) & 3) * 8 + (c >> 4) * 2 + ((c >> 3) & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           sum = s2.x + s2.y;
-          if (!S::two) break;
-          // head_dim <= 128: the weights were taken against the reference as it stood; if the
-          // block's maximum passes it too far, once more with the scores read again
-          const float mx = fmaf(raw, gk, fv);
-          const bool move = passes(mx);
-          if (__builtin_expect(!__any_sync(0xffffffffu, move), 1)) break;
-          move_to(move ? mx : m, k, j);
-          load_half(k, 0, x);
-          load_half(k, 1, x + 32);
-          tmem_wait_ld();
-          settle();
+          // head_dim <= 128: if the weights are too large for the reference as it stood, once
+          // more with the scores read again (a NaN among them comes here too, and stays)
+          move = !(sum <= kMaxSum);
+          if (__builtin_expect(!check || !__any_sync(0xffffffffu, move), 1)) break;
+          check = false;
+          load();
         }
         l = fmaf(sum, un, l);
         tmem_st32_async(tl + buf * 64, pk);
@@ -625,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the output
       const bool join = S::two && !pl.tiles;              // group 0 joins both lanes' outputs
-      const int slot = 2 * blockIdx.x + (g.first ? 0 : 1), tr = row - g.tile * S::rows;
+      const int slot = g.slot, tr = row - g.tile * S::rows;
       float k0 = 1.0f, k1 = 0.0f;
       if (join) {
         float2* x = reinterpret_cast<float2*>(xch);
