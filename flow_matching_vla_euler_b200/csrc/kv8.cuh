@@ -61,10 +61,12 @@ struct Kv8RowsParams {
   long long st_layer, st_row, st_tok;  // element strides of the bf16 side
   const int *slots, *pos, *count;
   int layer0, n_layers, batch, n_tokens, nblk_row;   // nblk_row: blocks a row can touch
+  int sm_count;
   int* err;
 };
 cudaError_t launch_kv8_write(const Kv8RowsParams& p, cudaStream_t s);
 cudaError_t launch_kv8_read(const Kv8RowsParams& p, cudaStream_t s);
+cudaError_t configure_kv8_store_kernels();
 cudaError_t launch_kv8_init(const Kv8Cache& c, cudaStream_t s);   // every scale to 2^-60
 
 struct Kv8AttendParams {

@@ -58,6 +58,7 @@ int kv8_rows(vla_kv8* h, const vla_kv8_rows* r, const void* K, const void* V, bo
   if (out && ((!p->st_tok && r->n_tokens > 1) || (!p->st_row && r->batch > 1) || (!p->st_layer && r->n_layers > 1)))
     return fail(VLA_ERR_ARG, "an output stride of 0");
   const int nb = (r->n_tokens + kKv8Block - 1) / kKv8Block;
+  p->sm_count = h->sm_count;
   p->nblk_row = std::min(h->c.nblk, r->pos ? (r->n_tokens + 2 * kKv8Block - 2) / kKv8Block : nb);
   const double units = static_cast<double>(r->n_layers) * r->batch * h->c.n_kv * p->nblk_row;
   if (units > 2147483647.0) return fail(VLA_ERR_SHAPE, "%.0f blocks in one call, at most 2^31 - 1", units);
@@ -118,6 +119,7 @@ int vla_kv8_create(const vla_kv8_config* cfg, vla_kv8** out) {
   if ((rc = dalloc(h, &h->ws, static_cast<size_t>(2) * sm_count * kv8_tc_rows(c) * c.Ds))) return cleanup(rc);
   if ((rc = dalloc(h, &h->ws_ml, static_cast<size_t>(2) * sm_count * kv8_tc_rows(c)))) return cleanup(rc);
   if ((rc = dalloc(h, &h->err, 1))) return cleanup(rc);
+  CU_CLEANUP(configure_kv8_store_kernels());
   CU_CLEANUP(configure_kv8_kernels());
   CU_CLEANUP(configure_kv8_tc_kernels());
   CU_CLEANUP(launch_kv8_init(c, 0));

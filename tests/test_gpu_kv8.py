@@ -2,19 +2,19 @@
 
 Stored values are compared bit for bit (a rounding to nearest of an exact quotient). The
 attention's bound, element by element: the output's own rounding to bf16, half a step =
-2^-8 |o|; the weights' rounding, at most 2^-8 of each (the coarser of the two kernels: two
-E4M3 terms, each off by half a step 2^-4), and the scores' error e_s, both of which reach o
-through sum p |v| / sum p:
+2^-8 |o|; the weights' rounding, at most 2^-8 of each (the coarser of the two kernels: bf16
+with many query rows, half a step 2^-8; fp16 with few, 2^-11), and the scores' error e_s, both
+of which reach o through sum p |v| / sum p:
     |err| <= 2^-8 |o| + (2^-8 + 2 e_s) * mean|v| (1 + 2^-7)
                  + 448 * 2^-22 * top + 2^-133
 with e_s = scale * ((D + 8) * 2^-23 * max_j sum_d |q_d k_jd| + 2^-17 max|q| max_j sum_d |k_jd|)
 + 2^-20 (fp32 sums of exact products, truncated at worst; Q as two E4M3 terms of a row scaled
 to a largest value in [128, 256), off by at most half of E4M3's smallest step, 2^-10; exp2
-and the subtraction of the maximum, 2^-20 in all). The last terms are the ends of the number
-ranges: a weight times its V scale is held relative to the largest of the row, which is at
-least 1, with a smallest step of 2^-21 (E4M3's second term: 2^-9 / 16 / 256; fp16's is 2^-24),
-so each of n keys adds at most 2^-22 of that largest times 448 (top = n * largest weight * V
-scale); bf16 ends at 2^-133.
+and the subtraction of the reference, 2^-20 in all). The last terms are the ends of the number
+ranges: fp16 weights are held relative to the largest of their block, with a smallest step of
+2^-24 (bf16's range has no such end here), so each of n keys adds less than 2^-22 of the
+largest weight times its V scale times 448 (top = n * largest weight * V scale); bf16 ends at
+2^-133.
 """
 import numpy as np
 import pytest
@@ -141,6 +141,43 @@ def test_token_by_token_equals_the_model():
                 slots=[1, 0])
         if t % 23 == 0 or t == 139:
             p.check_read(t + 1, batch=2)
+
+
+@pytest.mark.parametrize("L,kv,D", SHAPES)
+def test_short_writes_into_growing_blocks(L, kv, D):
+    """1 to 12 tokens a row (up to 8 have a kernel of their own) at odd positions, across a
+    block's end, with scales that grow, shrink and stay, and a broken token in some."""
+    rng = np.random.default_rng(D + 1)
+    p = Pair(L, kv, D, 190, 5)
+    pos = [0, 3, 60, 64, 127]
+    for step, n in enumerate([1, 8, 9, 2, 5, 12, 7, 1]):
+        f = [1.0, 30.0, 0.02, 500.0, 1e-3, 2e4, 1.0, 3e5][step]
+        K, Vv = f * kv_values(rng, (L, 4, n, kv * D)), f * kv_values(rng, (L, 4, n, kv * D))
+        if step in (2, 3, 4, 6):
+            (K if step & 1 else Vv)[L - 1, step % 4, n - 1, 7] = [np.nan, np.inf][step % 2]
+        slots = rng.permutation(5)[:4]
+        cnt = rng.integers(0, n + 1, 4)
+        cnt[step % 4] = n
+        p.write(K, Vv, pos=[pos[i] for i in slots], count=cnt, slots=slots)
+        for i, c in zip(slots, cnt):
+            pos[i] += int(c)
+        p.check_read(190, batch=5)
+
+
+@pytest.mark.parametrize("L,kv,D,B,n", [(2, 8, 32, 9, 1170), (3, 2, 64, 8, 1700), (5, 3, 128, 3, 1000),
+                                        (7, 2, 256, 3, 600)])
+def test_writes_of_more_blocks_than_run_at_once(L, kv, D, B, n):
+    """Every CTA takes several blocks in turn, some of them ragged, empty, broken or refused."""
+    rng = np.random.default_rng(n)
+    p = Pair(L, kv, D, n + 70, B)
+    cnt = [n] * B
+    cnt[1], cnt[2] = 0, n - 65
+    for pos in ([0, 5, 70][:3] + [1] * (B - 3), [64, 0, 7] + [70] * (B - 3)):
+        K, Vv = kv_values(rng, (L, B, n, kv * D)), kv_values(rng, (L, B, n, kv * D))
+        for t in range(3, n, 97):
+            (K if t & 1 else Vv)[t % L, t % B, t, t % (kv * D)] = np.nan
+        p.write(K, Vv, pos=pos, count=cnt, slots=list(range(B))[::-1])
+        p.check_read(n + 70, batch=B)
 
 
 def test_extreme_values():
@@ -451,3 +488,33 @@ def test_tensors_of_the_host_and_wrong_types_are_refused():
     c.close()
     with pytest.raises(V.VlaError):
         c.read(4)
+
+
+# ---------------------------------------------------------------- together with the pipeline
+
+def test_prefix_of_a_prefill_kept_in_the_cache_feeds_the_expert():
+    """An observation's prefix goes from the prefill into a slot of the cache, is attended there,
+    and comes back as the expert's prefix; the cache is the model's bit for bit, the actions are
+    the oracle's on the stored values."""
+    from vla_inputs import PREFILL_WORKLOADS, make_prefill_params, make_prefill_tokens
+    from ._helpers import check_actions, get, make_expert, oracle_actions, run
+    pwl, wl = PREFILL_WORKLOADS["prefill_tiny"], get("tiny")
+    L, n, D = pwl.cfg.n_layers, pwl.n_tokens, pwl.cfg.head_dim
+    pf = V.Prefill(pwl.cfg, make_prefill_params(pwl.cfg, pwl.seed), max_tokens=n)
+    K, Vv = pf.run(torch.from_numpy(make_prefill_tokens(pwl)).cuda())
+    p = Pair(L, 1, D, n + 3, 4)
+    p.c.write(K, Vv, slots=i32([2]))
+    p.m.write(host(K), host(Vv), slots=[2])
+    p.check_read(n, slots=[2])
+    rng = np.random.default_rng(11)
+    for l in range(L):
+        p.check_attend(rng.standard_normal((1, 5, wl.expert.n_heads, D)), [n], slots=[2], layer=l)
+    Kb, Vb = p.c.read(n, slots=i32([2]))
+    ex, inp = make_expert(wl)
+    ex.set_prefix(Kb, Vb)
+    got = run(ex, inp, wl.steps)
+    ref = oracle_actions(wl, inp, prefix_k=Kb.cpu().numpy().view(np.uint16), prefix_v=Vb.cpu().numpy().view(np.uint16))
+    check_actions(got, ref, "expert on the stored prefix")
+    p.c.status()
+    ex.close()
+    pf.close()
