@@ -266,6 +266,12 @@ __device__ __forceinline__ bool kv8_next(const Kv8AttendParams& p, Kv8Walk& w, K
   return true;
 }
 
+// The merges look for the cuts of each item, if there are fewer items than cuts and a warp holds
+// all entries; else for the item of each cut.
+__host__ __device__ __forceinline__ bool kv8_merge_by_items(const Kv8AttendParams& p) {
+  return p.batch * p.tiles <= 128 && p.batch * p.tiles * p.c.n_kv < p.grid - 1;
+}
+
 // Few rows (tile_rows 8 or 16) and many (128 or 256).
 cudaError_t launch_kv8_attend_rows(const Kv8AttendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_attend_tc(const Kv8AttendParams& p, cudaStream_t s);

@@ -210,7 +210,11 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   p.ws = h->ws;
   p.ws_ml = h->ws_ml;
   const double rows = static_cast<double>(a->n_q) * p.group;
-  const bool few = rows <= 16;
+  // One tile of 16 rows: the kernel for few rows. Two: also, if there are so few of them that its
+  // shorter start counts for more than reading the keys twice (20 rows of head_dim 128, 8 K/V heads,
+  // few and many: 4 x 512 keys 24.5 and 30.2 us, 4 x 4096 36.9 and 47.1, 16 x 4096 86.0 and 77.8; 32
+  // rows of head_dim 256, 32 x 788 41.0 and 45.1, 64 x 788 57.3 and 43.0).
+  const bool few = rows <= 16 || (rows <= 32 && static_cast<double>(a->batch) * h->c.n_kv <= 32);
   p.tile_rows = rows <= 8 ? 8 : few ? 16 : kv8_tc_rows(h->c);
   const double tiles = std::ceil(rows / p.tile_rows);
   const double units = tiles * h->c.n_kv * a->batch * h->c.nblk;

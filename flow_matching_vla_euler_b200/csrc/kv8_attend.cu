@@ -417,29 +417,51 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
 
 // ---- merging the parts of the items that more than one CTA worked on
 
-// The item that the cut before part `cut` lies in, if it is the first cut that stays inside that item.
+// An item with cuts inside.
 struct Kv8Cut {
   int b, tile, head, rows;      // rows: query rows of the tile
   int c0, c1;                   // parts c0 .. c1 - 1 meet the item
 };
-__device__ __forceinline__ bool kv8_cut(const Kv8AttendParams& p, const Kv8Line& line, int cut, Kv8Cut& r) {
+// Of item `head` of entry e, which begins with unit u0 and has cuts from `cut` on inside if any.
+__device__ __forceinline__ bool kv8_parts(const Kv8AttendParams& p, const Kv8Line& line, const Kv8Tile& row, int e,
+                                          int head, int u0, int cut, Kv8Cut& r) {
+  // cuts of [u0 + snap + 1, u1 - snap - 1] stay
+  const int lo = u0 + line.snap, hi = u0 + row.units - line.snap;
   const int uc = kv8_begin(line, cut);
+  if (cut >= p.grid || uc <= lo || uc >= hi || kv8_begin(line, cut - 1) > lo) return false;
+  r.b = p.by_tiles.div(e);
+  r.tile = e - r.b * p.tiles;
+  r.head = head;
+  r.rows = min(p.tile_rows, row.cnt * p.group - r.tile * p.tile_rows);
+  r.c0 = cut - 1;
+  // (parts that meet the item have units: the cuts inside an item differ)
+  r.c1 = min(p.grid, cut + (line.per > 0 ? (hi - uc - 1) / line.per + 1 : hi - uc));
+  while (r.c1 > cut && kv8_begin(line, r.c1 - 1) >= hi) --r.c1;
+  return true;
+}
+// The merges' second grid axis: the items, or the cuts where these are fewer (an item belongs to
+// the first cut that stays inside it).
+__device__ __forceinline__ bool kv8_cut(const Kv8AttendParams& p, const Kv8Line& line, int y, Kv8Cut& r) {
+  if (kv8_merge_by_items(p)) {
+    const int e = y / p.c.n_kv, head = y - e * p.c.n_kv;
+    const int b = p.by_tiles.div(e);
+    const Kv8Tile row = kv8_tile(p, b, e - b * p.tiles);
+    if (row.units == 0) return false;
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (32 * i + static_cast<int>(threadIdx.x & 31) < e) before += line.w[i];
+    const int u0 = __reduce_add_sync(0xffffffffu, before) + head * row.units;
+    int cut = max(1, (u0 + line.snap) / (line.per + 1));
+    while (cut < p.grid && kv8_begin(line, cut) <= u0 + line.snap) ++cut;
+    return kv8_parts(p, line, row, e, head, u0, cut, r);
+  }
+  const int cut = y + 1, uc = kv8_begin(line, cut);
   if (uc >= line.total) return false;
   int inside;
   const int e = kv8_find(p, line, uc, &inside);
   const Kv8Tile row = kv8_tile(p, p.by_tiles.div(e), p.by_tiles.mod(e));
-  // cuts of [u0 + snap + 1, u1 - snap - 1] stay
-  const int u0 = uc - inside % row.units + line.snap, u1 = u0 + row.units - 2 * line.snap;
-  if (uc <= u0 || uc >= u1 || kv8_begin(line, cut - 1) > u0) return false;
-  r.b = p.by_tiles.div(e);
-  r.tile = e - r.b * p.tiles;
-  r.head = inside / row.units;
-  r.rows = min(p.tile_rows, row.cnt * p.group - r.tile * p.tile_rows);
-  r.c0 = cut - 1;
-  // (parts that meet the item have units: the cuts inside an item differ)
-  r.c1 = min(p.grid, cut + (line.per > 0 ? (u1 - uc - 1) / line.per + 1 : u1 - uc));
-  while (r.c1 > cut && kv8_begin(line, r.c1 - 1) >= u1) --r.c1;
-  return true;
+  return kv8_parts(p, line, row, e, inside / row.units, uc - inside % row.units, cut, r);
 }
 
 constexpr int kMergeWarps = 8;
@@ -457,7 +479,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_rows_kernel(const 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x;
   const Kv8Line line = kv8_line(p);
   Kv8Cut cut;
-  const bool mine = kv8_cut(p, line, blockIdx.y + 1, cut);
+  const bool mine = kv8_cut(p, line, blockIdx.y, cut);
   pdl_wait();
   if (!mine || r >= cut.rows) return;
   float mm = -INFINITY, ll = 0.0f;
@@ -546,7 +568,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_tiles_kernel(const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x * 32 + lane;
   const Kv8Line line = kv8_line(p);
   Kv8Cut cut;
-  const bool mine = kv8_cut(p, line, blockIdx.y + 1, cut);
+  const bool mine = kv8_cut(p, line, blockIdx.y, cut);
   pdl_wait();
   if (!mine || r >= cut.rows) return;
   float mm = -INFINITY, ll = 0.0f;
@@ -588,11 +610,82 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_tiles_kernel(const
         ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
-cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
+// Many rows in many parts (few items, so that many CTAs share each): a CTA per (32 rows, item, 32
+// columns); a lane is a row, a warp takes every eighth part, and the eight sums are joined in
+// order in shared memory. (Row by row of parts, as above, 128 parts of 128 rows of 256 took 200 us.)
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_parts_kernel(const Kv8AttendParams p) {
+  constexpr int W = kMergeWarps;
+  __shared__ float2 sml[W][32];
+  __shared__ float4 so[W][8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x * 32 + lane, g0 = blockIdx.z * 8;
+  const Kv8Line line = kv8_line(p);
+  Kv8Cut cut;
+  const bool mine = kv8_cut(p, line, blockIdx.y, cut);
+  pdl_wait();
+  if (!mine || static_cast<int>(blockIdx.x) * 32 >= cut.rows) return;
+  float mm = -INFINITY, ll = 0.0f;
+  float4 v[8] = {};
+  if (r < cut.rows)
+#pragma unroll 2
+    for (int c = cut.c0 + warp; c < cut.c1; c += W) {
+      const int slot = kv8_slot(c, c == cut.c0);
+      const float2 ml = p.ws_ml[slot * p.tile_rows + r];
+      const float4* x = reinterpret_cast<const float4*>(p.ws + static_cast<size_t>(slot) * p.tile_rows * D) + r;
+      const float nm = fmaxf(mm, ml.x);
+      const float k = mm == -INFINITY ? 1.0f : exp2_approx(mm - nm), f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - nm);
+      mm = nm;
+      ll = fmaf(ml.y, f, ll * k);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 y = x[(g0 + j) * p.tile_rows];
+        v[j] = make_float4(fmaf(y.x, f, v[j].x * k), fmaf(y.y, f, v[j].y * k), fmaf(y.z, f, v[j].z * k),
+                           fmaf(y.w, f, v[j].w * k));
+      }
+    }
+  sml[warp][lane] = make_float2(mm, ll);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) so[warp][j][lane] = v[j];
+  __syncthreads();
+  if (r >= cut.rows) return;
+  // this warp's four columns of the row
+  mm = sml[0][lane].x;
+#pragma unroll
+  for (int i = 1; i < W; ++i) mm = fmaxf(mm, sml[i][lane].x);
+  ll = 0.0f;
+  float4 o = {};
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float2 y = sml[i][lane];
+    const float k = y.x == -INFINITY ? 1.0f : exp2_approx(y.x - mm);
+    const float4 z = so[i][warp][lane];
+    ll = fmaf(y.y, k, ll);
+    o = make_float4(fmaf(z.x, k, o.x), fmaf(z.y, k, o.y), fmaf(z.z, k, o.z), fmaf(z.w, k, o.w));
+  }
+  const int q = cut.tile * p.tile_rows + r;
+  const int qi = p.by_group.div(q), qh = cut.head * p.group + p.by_group.mod(q);
+  const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
+  const int d = (g0 + warp) * 4;
+  if (d < p.c.D) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * norm, o.y * norm);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * norm, o.w * norm);
+    *reinterpret_cast<uint2*>(p.out + cut.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2] + d) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  if (d == 0 && p.lse)
+    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] =
+        ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+}
+
+template <int D>
+static cudaError_t launch_merge(const Kv8AttendParams& p, cudaStream_t s) {
   if (p.grid < 2) return cudaSuccess;
-  const bool few = p.tile_rows <= 16;
+  const bool few = p.tile_rows <= 16, by_items = kv8_merge_by_items(p);
+  const int items = p.batch * p.tiles * p.c.n_kv;
+  // more than eight CTAs to an item
+  const bool parts = !few && by_items && items * 8 < p.grid;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(few ? p.tile_rows : p.tile_rows / 32, p.grid - 1);
+  cfg.gridDim = dim3(few ? p.tile_rows : p.tile_rows / 32, by_items ? items : p.grid - 1, parts ? D / 32 : 1);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute a[1];
@@ -600,10 +693,15 @@ cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<D> : parts ? kv8_merge_parts_kernel<D>
+                                                                          : kv8_merge_tiles_kernel<D>, p);
+}
+
+cudaError_t launch_kv8_merge(const Kv8AttendParams& p, cudaStream_t s) {
   switch (p.c.Ds) {
-    case 64: return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<64> : kv8_merge_tiles_kernel<64>, p);
-    case 128: return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<128> : kv8_merge_tiles_kernel<128>, p);
-    default: return cudaLaunchKernelEx(&cfg, few ? kv8_merge_rows_kernel<256> : kv8_merge_tiles_kernel<256>, p);
+    case 64: return launch_merge<64>(p, s);
+    case 128: return launch_merge<128>(p, s);
+    default: return launch_merge<256>(p, s);
   }
 }
 

@@ -255,6 +255,15 @@ def test_groups_of_heads(group):
     p.check_attend(rng.standard_normal((3, 1, 2 * group, 64)), [150, 1, 129], slots=[2, 2, 0], causal=True)
 
 
+@pytest.mark.parametrize("kv,B,rows", [(4, 8, 32), (4, 8, 33), (11, 3, 32), (11, 3, 20), (1, 32, 17)])
+def test_both_sides_of_the_choice_of_kernel(kv, B, rows):
+    rng = np.random.default_rng(rows)
+    p = _filled(rng, kv, 64, 130, B)
+    lens = rng.integers(0, 131, B)
+    p.check_attend(rng.standard_normal((B, rows, kv, 64)), lens, causal=True)
+    p.check_attend(rng.standard_normal((B, rows, kv, 64)), lens, causal=True, window=40)
+
+
 @pytest.mark.parametrize("D,kv,H,nq", [(64, 4, 20, 5), (128, 2, 8, 50), (256, 1, 8, 50), (32, 1, 4, 17), (256, 2, 2, 7),
                                        (128, 1, 3, 129), (64, 1, 1, 300)])
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 37), (False, 200)])
@@ -283,6 +292,18 @@ def test_long_row_over_many_parts():
     p.check_attend(rng.standard_normal((2, 1, 4, 64)), [20000, 77])
     p.check_attend(rng.standard_normal((2, 1, 4, 64)), [64, 19999], scale=0.5)
     p.check_attend(rng.standard_normal((2, 2, 20, 64)), [9999, 19999], causal=True, window=9000)
+
+
+@pytest.mark.parametrize("D,kv,H,nq,B,window", [(256, 1, 8, 5, 1, 0), (256, 1, 8, 17, 2, 0), (128, 2, 8, 9, 1, 0),
+                                                (128, 1, 4, 100, 3, 0), (64, 1, 20, 13, 1, 2500), (32, 3, 3, 65, 2, 0)])
+def test_few_items_over_all_ctas(D, kv, H, nq, B, window):
+    """Items whose blocks are spread over many CTAs, with a length that leaves one a single
+    block and (three rows) an empty one."""
+    rng = np.random.default_rng(nq)
+    n = 5200
+    p = _filled(rng, kv, D, n, B)
+    lens = [n, 40, 0][:B]
+    p.check_attend(rng.standard_normal((B, nq, H, D)), lens, causal=True, window=window)
 
 
 def test_scores_of_unlike_size():
