@@ -30,6 +30,12 @@
 //     output of its own; the two outputs are joined at the end.
 //   head_dim 256: lane i takes every second block; one output (256 columns), for which the row's
 //     reference maximum goes from block to block between the two groups.
+// 2 x 2048 queries of 32 heads (8 K/V heads, head_dim 128) behind 4096 stored tokens: 0.41 ms, 49 %
+// of the measured bf16 rate counted on the formula's products. Per SM a step of 64 keys for both
+// tiles takes 2500 clocks; its parts alone take 1280 (tensor pipe: the scores' operands come from
+// shared memory at 48 clocks a product of 64 keys, 8 a tile; 4 of 64 clocks for the output), 1060
+// (exponentials) and 1350 (shared memory). The rest is the way from scores to weights to the next
+// scores of a buffer, of which tensor memory holds two a tile beside the outputs and no more.
 // Warps: 0 and 1 scores, 2 and 3 outputs of lane 0 and 1, 4..7 and 8..11 softmax of lane 0 and 1
 // (one thread a row), 12..15 widening of V, 16 loads of K, 17 loads of V.
 #include <float.h>
@@ -48,7 +54,7 @@ constexpr int kThreads = 640;
 
 // The reference moves when a block's largest exponent is above it by more than kLag (head_dim
 // 256), its weights sum to more than kMaxSum (else). A row's sum of exponentials leaves the V
-// scale (>= 2^-60) out of its terms: 2^40 or 64 times 2^32, times 2^60, times 2^20 blocks stay below 2^127.
+// scale (>= 2^-60) out of its terms: 2^40 or 64 times 2^32, times 2^60, times 2^24 blocks stay below 2^127.
 constexpr float kLag = 32.0f, kMaxSum = 1099511627776.0f;
 
 template <int D>

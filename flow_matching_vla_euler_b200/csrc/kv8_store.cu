@@ -7,6 +7,11 @@
 // even. A write that begins inside a block keeps the block's earlier tokens: its scale can
 // only grow, and the kept tokens move by an exact shift of exponents (only values that reach
 // E4M3's subnormals round again).
+//
+// Bound by memory: three bytes a value in each direction (two of bf16, one of the cache). Whole
+// blocks are 82 % (64 x 18 x 788 tokens of 256 written and read back, 522 us) and 98 % (32 ragged
+// rows of up to 4096 tokens of 8 x 128, 4 layers, read in 376 us) of the copy rate. Writes alone
+// take 268 us of the 522, 79 %: their 32 registers of data a thread leave 32 warps an SM.
 #include <algorithm>
 
 #include "kernels.h"
@@ -132,8 +137,8 @@ constexpr int kWriteSmem = 2 * D * 128;  // pieces in flight
 // 2t+9 of a 16-token group) in 8 registers of 16 bytes: the data is read once, and the maximum
 // and the rounding work on registers. A CTA takes every gridDim-th unit; while it works on one,
 // each thread's pieces of the next are on their way to a place of its own in shared memory, so
-// that loads are always in flight (with one unit a CTA and no loads ahead: 318 us for
-// 64 x 18 x 788 tokens of 256, 212 at the copy rate).
+// that loads are always in flight. 64 x 18 x 788 tokens of 256: 318 us with one unit a CTA, no loads
+// ahead and 877 instructions a warp, 268 us so (560 instructions), 212 at the copy rate.
 template <int D>
 __global__ void __launch_bounds__(2 * D, kWriteCtas<D>) kv8_write_kernel(const Kv8RowsParams p, const unsigned units) {
   constexpr int kVec = D / 8;              // 16-byte pieces of a token
@@ -313,28 +318,34 @@ __global__ void __launch_bounds__(2 * D, kWriteCtas<D>) kv8_write_kernel(const K
 }
 
 // A write of a few tokens a row (decoding): a CTA per unit, a thread per dim of K and V, so that
-// all units of an ordinary append are on the chip at once (2 D threads with 64 registers: 29 us
-// for one token of 64 x 18 rows of 256, most of it waiting in four waves). The bytes go straight to
-// their places; a block's other bytes are touched only when its scale has to grow.
+// the units of an ordinary append are on the chip at once: one token of 64 x 18 rows of 256 in
+// 16 us, 29 us with the kernel above, whose blocks wait in four waves. The bytes go straight to their
+// places; a block's other bytes are touched only when its scale has to grow. What is left is the
+// latency of lengths, rows and scales one after the other.
 constexpr int kFewTokens = 8;
 template <int D>
 __global__ void __launch_bounds__(D) kv8_write_few_kernel(const Kv8RowsParams p) {
   constexpr int kDs = D < 64 ? 64 : D;
   constexpr int kWarps = D / 32;
   __shared__ uint32_t red[kWarps][2][kFewTokens];
+  __shared__ WriteUnit unit;
   const int d = threadIdx.x;
-  const WriteUnit u = write_unit(p, blockIdx.x, D);      // (the same in every warp)
+  if (d < 32) {
+    const WriteUnit a = write_unit(p, blockIdx.x, D);
+    if (d == 0) unit = a;
+  }
+  __syncthreads();
+  const WriteUnit u = unit;
   if (u.lo >= u.hi) return;
   const int n = u.hi - u.lo;
   const long long at = u.src + u.lo * p.st_tok + d;
-  uint32_t x[2][kFewTokens];
+  uint32_t x[kFewTokens];                  // K, V << 16
 #pragma unroll
   for (int i = 0; i < kFewTokens; ++i) {
-    x[0][i] = x[1][i] = 0;
-    if (i < n) {
-      x[0][i] = reinterpret_cast<const uint16_t*>(p.k_in)[at + i * p.st_tok];
-      x[1][i] = reinterpret_cast<const uint16_t*>(p.v_in)[at + i * p.st_tok];
-    }
+    x[i] = 0;
+    if (i < n)
+      x[i] = reinterpret_cast<const uint16_t*>(p.k_in)[at + i * p.st_tok] |
+             static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.v_in)[at + i * p.st_tok]) << 16;
   }
   float4* sc = p.c.scale + u.idx;
   const float2 old_s = u.lo > 0 ? *reinterpret_cast<const float2*>(sc) : make_float2(0.0f, 0.0f);
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(D) kv8_write_few_kernel(const Kv8RowsParams p)
     if (i < n)
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, x[kv][i] & 0x7fffu);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, x[i] >> (16 * kv) & 0x7fffu);
         if ((d & 31) == 0) red[d >> 5][kv][i] = m;
       }
   __syncthreads();
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(D) kv8_write_few_kernel(const Kv8RowsParams p)
     for (int i = 0; i < kFewTokens; ++i)
       if (i < n) {
         const int tok = u.lo + i;
-        uint8_t q = static_cast<uint8_t>(f2_to_e4m3x2(__uint_as_float(x[kv][i] << 16) * inv, 0.0f));
+        uint8_t q = static_cast<uint8_t>(f2_to_e4m3x2((kv ? bf_hi(x[i]) : bf_lo(x[i])) * inv, 0.0f));
         if (broken >> i & 1) q = kv ? 0 : 0x7f;
         if (kv) {                          // token 16 w + 8 h + 2 t + e is byte 16 t + 4 w + 2 h + e of its dim
           blk[kv8_chunk(d, (tok >> 1) & 3) + 4 * (tok >> 4) + 2 * ((tok >> 3) & 1) + (tok & 1)] = q;
@@ -407,7 +418,8 @@ __global__ void __launch_bounds__(D) kv8_write_few_kernel(const Kv8RowsParams p)
   }
 }
 
-// 2 D threads, halves and token quads as in the write. Values are exact in bf16 (E4M3 has
+// 2 D threads, halves and token quads as in the write, and 32 registers a thread, so that an SM is
+// full (with 40: 397 us for the ragged rows above, 376 so). Values are exact in bf16 (E4M3 has
 // four significant bits, the scale is a power of two).
 template <int D>
 __global__ void __launch_bounds__(2 * D, 1024 / D) kv8_read_kernel(const Kv8RowsParams p) {

@@ -322,6 +322,21 @@ def test_scores_of_unlike_size():
     zero.check_attend(Q[:, :3], [400])
 
 
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 9, 70])
+def test_scores_that_climb_from_block_to_block(D, nq):
+    """Each block's scores pass the last one's by far (and fall back), so that every reference
+    moves again and again; a row's first blocks lie outside its window."""
+    rng = np.random.default_rng(D + nq)
+    p = Pair(1, 1, D, 64 * 12, 2)
+    f = np.repeat([1.0, 40.0, 300.0, 3.0, 2000.0, 9000.0, 0.1, 3e4, 1e5, 7.0, 2e5, 1.0], 64)
+    K, Vv = (rng.standard_normal((1, 2, 64 * 12, D)) for _ in range(2))
+    p.write(K * f[:, None], Vv * f[::-1, None])
+    Q = rng.standard_normal((2, nq, 4, D))
+    p.check_attend(Q, [64 * 12, 64 * 9 - 5])
+    p.check_attend(Q, [64 * 12, 64 * 9 - 5], causal=True, window=300)
+
+
 def test_strided_queries_and_outputs():
     rng = np.random.default_rng(6)
     p = _filled(rng, 2, 64, 100, 3)
@@ -374,6 +389,23 @@ def test_rows_out_of_range_are_left_out_and_reported():
         assert torch.all(out[1:] == 7.0)
         ref, _, mean_v, _, _ = fresh.m.attend(qn[:1], [100])
         assert np.all(np.abs(host(out[:1]) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7.9 * mean_v)
+
+
+@pytest.mark.parametrize("n", [1, 8, 9])
+def test_refused_rows_of_short_and_long_writes(n):
+    rng = np.random.default_rng(n)
+    p = _filled(rng, 2, 128, 100, 4)
+    K, kn = bf16(kv_values(rng, (1, 5, n, 256)))
+    # row 1 names a slot twice, row 2 one that is not there, row 4 runs over the end
+    p.c.write(K, K, slots=i32([3, 3, 4, 0, 1]), pos=i32([60, 5, 0, 63, 101 - n]))
+    for r, slot, pos in ((0, 3, 60), (3, 0, 63)):
+        p.m.write(kn[:, r:r + 1], kn[:, r:r + 1], slots=[slot], pos=[pos])
+    with pytest.raises(V.VlaError) as ei:
+        p.c.status()
+    assert ei.value.code == V.VLA_ERR_SHAPE
+    p.check_read(60 + n, slots=[3])
+    p.check_read(63 + n, slots=[0])
+    p.check_read(100, slots=[1, 2])
 
 
 def test_captured_calls_follow_the_device_arrays():
