@@ -31,11 +31,11 @@
 //   head_dim 256: lane i takes every second block; one output (256 columns), for which the row's
 //     reference maximum goes from block to block between the two groups.
 // 2 x 2048 queries of 32 heads (8 K/V heads, head_dim 128) behind 4096 stored tokens: 0.41 ms, 49 %
-// of the measured bf16 rate counted on the formula's products. Per SM a step of 64 keys for both
-// tiles takes 2500 clocks; its parts alone take 1280 (tensor pipe: the scores' operands come from
-// shared memory at 48 clocks a product of 64 keys, 8 a tile; 4 of 64 clocks for the output), 1060
-// (exponentials) and 1350 (shared memory). The rest is the way from scores to weights to the next
-// scores of a buffer, of which tensor memory holds two a tile beside the outputs and no more.
+// of the measured bf16 rate counted on the formula's products. A step of 64 keys for both tiles
+// takes 1.1 us (2100 clocks) of an SM at head_dim 128 and 1.05 at 64, so it is not the products that
+// bound it: the softmax groups' way through a step does, of which the exponentials fill half (1030
+// clocks for two warps a scheduler) and the loads, stores and waits of a warp the rest. Each new tile
+// costs 8 us more (Q, start of the lanes, output) and a part of one the merge.
 // Warps: 0 and 1 scores, 2 and 3 outputs of lane 0 and 1, 4..7 and 8..11 softmax of lane 0 and 1
 // (one thread a row), 12..15 widening of V, 16 loads of K, 17 loads of V.
 #include <float.h>
@@ -118,6 +118,20 @@ __device__ __forceinline__ void umma_commit_if(uint32_t lead, uint32_t bar) {
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(lead), "r"(bar)
       : "memory");
+}
+// A bounded wait of a whole converged warp. What depends on it, like every choice of the softmax
+// groups that is the same for a warp, goes through a vote, so that the compiler keeps no path for
+// lanes that part (406 -> 397 us for 2 x 2048 queries behind 4096 tokens).
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+      report(err, kDevTimeout);
+      return false;
+    }
+  }
 }
 // Two fp32 lanes in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -505,10 +519,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       kv8_seen(p, g.row, p.by_group.div(r0 + max(rows, 1) - 1), lo_last, t1);
       const float4* scales = p.c.scale +
           ((static_cast<size_t>(p.layer) * p.c.n_slots + g.row.slot) * p.c.n_kv + g.head) * p.c.nblk + g.blk;
-      const int steps = pl.steps[grp];
+      const int steps = grp ? pl.steps[1] : pl.steps[0];   // (no array indexed at run time: local memory)
       const int stride = pl.tiles ? 1 : 2, first = pl.tiles ? 0 : grp;   // block of step k: first + k * stride
-      auto scale_of = [&](int k) { return __ldg(scales + min(first + k * stride, g.n - 1)); };
-      float4 sc = scale_of(0);
+      auto scale_of = [&](int k) {
+        return __ldg(reinterpret_cast<const float2*>(scales + min(first + k * stride, g.n - 1)));
+      };
+      float2 sc = scale_of(0);
       float m = -INFINITY, l = 0.0f;
       // moves the row's reference to nm, and with it l and (if it has begun) this warp's rows of O:
       // after the last product on them
@@ -535,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int k = 0; k < steps; ++k) {
         const int buf = 2 * grp + (k & 1), j = first + k * stride, key0 = (g.blk + j) * kKv8Block;
-        ok = ok && mbar_wait(sfull + 8 * buf, buf_parity(ph, grp, k), p.err);
+        ok = ok && wait_warp(sfull + 8 * buf, buf_parity(ph, grp, k), p.err);
         tc_fence_after();
         const float gk = fmaxf(rowf * sc.x, FLT_MIN);       // (never 0: a masked score stays -infinity)
         const int ev = exp_of(sc.y);
@@ -548,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(x[c]));   // x is not used before the wait
-          if (__builtin_expect(key0 < lo_last || key0 + 64 > hi_first, 0)) {
+          if (__builtin_expect(__any_sync(0xffffffffu, key0 < lo_last || key0 + 64 > hi_first), 0)) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c < lo - key0 || c >= hi - key0) x[c] = -INFINITY;
