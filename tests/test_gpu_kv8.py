@@ -408,6 +408,57 @@ def test_refused_rows_of_short_and_long_writes(n):
     p.check_read(100, slots=[1, 2])
 
 
+@pytest.mark.parametrize("nq", [1, 3, 40])
+@pytest.mark.parametrize("D", [64, 256])
+def test_queries_that_are_not_finite_touch_their_own_rows_only(D, nq):
+    rng = np.random.default_rng(nq)
+    p = _filled(rng, 1, D, 300, 2)
+    Q = rng.standard_normal((3, nq, 8, D))
+    Q[0, 0, 2, 5], Q[1, nq - 1, 7, 0], Q[2, nq // 2, 0] = np.nan, np.inf, -np.inf
+    _, got, ls = p.attend(Q, [300, 64, 300], slots=[1, 0, 1], causal=True)
+    bad = np.zeros(Q.shape[:3], bool)
+    bad[0, 0, 2] = bad[1, nq - 1, 7] = bad[2, nq // 2, 0] = True
+    assert np.isnan(got[bad]).all() and np.isnan(ls[bad]).all()
+    Q[bad] = 0.0
+    _, clean, lc = p.attend(Q, [300, 64, 300], slots=[1, 0, 1], causal=True)
+    assert np.array_equal(got[~bad], clean[~bad]) and np.array_equal(ls[~bad], lc[~bad])
+    p.check_attend(Q, [300, 64, 300], slots=[1, 0, 1], causal=True)
+
+
+def test_offsets_past_32_bits():
+    """A cache of 2 x 4.6 GB, its last slot; K and V rows 2^31 elements apart."""
+    rng = np.random.default_rng(1)
+    D, cap, S, n = 256, 100000, 180, 70
+    c = V.KVCache8(n_layers=1, n_kv_heads=1, head_dim=D, capacity=cap, n_slots=S)
+    m = O.Kv8Model(1, 1, D, 2 * n, 2)
+    base = torch.empty(2 ** 31 + n * D, dtype=torch.bfloat16, device="cuda")
+    K = base.as_strided((1, 2, n, D), (8, 2 ** 31, D, 1))
+    x, xn = bf16(kv_values(rng, (1, 2, n, D)))
+    K.copy_(x)
+    pos = [cap - 2 * n, 64 * 1500]
+    c.write(K, K, slots=i32([S - 1, S - 2]), pos=i32(pos))
+    c.write(K[:, :, :3], K[:, :, :3], slots=i32([S - 1, S - 2]), pos=i32([p + n for p in pos]))
+    o, o2 = (torch.zeros_like(base).as_strided((1, 2, n, D), (8, 2 ** 31, D, 1)) for _ in range(2))
+    c.read(n, slots=i32([S - 1, S - 2]), pos=i32(pos), K_out=o, V_out=o2)
+    c.status()
+    # the first row begins inside a block (of zeros until then), the second with one
+    off = pos[0] % 64
+    m.write(xn[:, :1], xn[:, :1], slots=[0], pos=[off])
+    m.write(xn[:, 1:], xn[:, 1:], slots=[1])
+    m.write(xn[:, :1, :3], xn[:, :1, :3], slots=[0], pos=[off + n])
+    m.write(xn[:, 1:, :3], xn[:, 1:, :3], slots=[1], pos=[n])
+    np.testing.assert_array_equal(host(o[0, 0]), m.read(0, n, slots=[0], pos=[off])[0, 0])
+    np.testing.assert_array_equal(host(o2[0, 0]), m.read(1, n, slots=[0], pos=[off])[0, 0])
+    np.testing.assert_array_equal(host(o[0, 1]), m.read(0, n, slots=[1])[0, 0])
+    for nq in (1, 30):                               # the last n + 3 tokens by their window
+        q, qn = bf16(rng.standard_normal((2, nq, 8, D)))
+        out = c.attend(q, i32([p + n + 3 for p in pos]), slots=i32([S - 1, S - 2]), causal=True, window=n + 3 - nq)
+        ref, _, mean_v, _, _ = m.attend(qn, [off + n + 3, n + 3], slots=[0, 1], causal=True, window=n + 3 - nq)
+        assert np.all(np.abs(host(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7.5 * mean_v)
+    c.status()
+    c.close()
+
+
 def test_captured_calls_follow_the_device_arrays():
     """A captured append and attend, replayed as the positions move on; bit-identical to the
     same calls made one by one."""
