@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(qd * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + S::xch);
     uint32_t ph = 0;
+    bool up = true;                      // no wait for scores gave up: the same in a whole warp, unlike ok
     while (kv8_next(p, w, g)) {
       const Plan pl = make_plan<D>(p, g);
       const int left = g.row.cnt * p.group - g.tile * S::rows;      // rows from the tile's first on
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         const int before = S::two ? k - 1 : (j - 1) >> 1, of = S::two ? grp : grp ^ 1;
         if ((S::two ? k : j) > 0) {
-          ok = ok && mbar_wait(odone + 8 * (2 * of + (before & 1)), buf_parity(ph, of, before), p.err);
+          ok = ok && up && mbar_wait(odone + 8 * (2 * of + (before & 1)), buf_parity(ph, of, before), p.err);
           tc_fence_after();
           const uint32_t to = tl + S::o_col + (S::two ? grp * D : 0);
 #pragma unroll 1
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int k = 0; k < steps; ++k) {
         const int buf = 2 * grp + (k & 1), j = first + k * stride, key0 = (g.blk + j) * kKv8Block;
-        ok = ok && wait_warp(sfull + 8 * buf, buf_parity(ph, grp, k), p.err);
+        up = up && wait_warp(sfull + 8 * buf, buf_parity(ph, grp, k), p.err);
         tc_fence_after();
         const float gk = fmaxf(rowf * sc.x, FLT_MIN);       // (never 0: a masked score stays -infinity)
         const int ev = exp_of(sc.y);
@@ -665,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the last products on the outputs read here. A wait may look one phase ahead only, so the
         // groups of head_dim 256 wait for the last two blocks in order.
         if (S::two) {
-          ok = ok && mbar_wait(odone + 8 * (2 * grp + ((steps - 1) & 1)), buf_parity(ph, grp, steps - 1), p.err);
+          ok = ok && up && mbar_wait(odone + 8 * (2 * grp + ((steps - 1) & 1)), buf_parity(ph, grp, steps - 1), p.err);
           if (join && pl.steps[1] > 0) {
             const int e = pl.steps[1] - 1;
-            ok = ok && mbar_wait(odone + 8 * (2 + (e & 1)), buf_parity(ph, 1, e), p.err);
+            ok = ok && up && mbar_wait(odone + 8 * (2 + (e & 1)), buf_parity(ph, 1, e), p.err);
           }
         } else {
           for (int t = max(0, g.n - 2); t < g.n; ++t)
-            ok = ok && mbar_wait(odone + 8 * (2 * (t & 1) + ((t >> 1) & 1)), buf_parity(ph, t & 1, t >> 1), p.err);
+            ok = ok && up && mbar_wait(odone + 8 * (2 * (t & 1) + ((t >> 1) & 1)), buf_parity(ph, t & 1, t >> 1), p.err);
         }
         tc_fence_after();
         const bool have1 = join && pl.steps[1] > 0;
