@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           const uint8_t* src = smem + S::v8 + r * D * 64;
           uint8_t* dst = smem + S::v16 + r * D * 128;
-#pragma unroll 2
+#pragma unroll 4
           for (int i = tid; i < D * 4; i += 128) {
             const int d = i >> 2, c = i & 3;
             const uint4 x = *reinterpret_cast<const uint4*>(src + d * 64 + ((c ^ ((d >> 1) & 3)) << 4));
