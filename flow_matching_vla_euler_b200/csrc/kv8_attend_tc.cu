@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t kfull = sm + S::bar, kempty = kfull + 8 * S::nk;
   const uint32_t rfull = kempty + 8 * S::nk, rempty = rfull + 8 * S::nv;      // V as stored
   const uint32_t vfull = rempty + 8 * S::nv, vempty = vfull + 8 * S::nv;      // V widened
-  const uint32_t sfull = vempty + 8 * S::nv, pfull = sfull + 32, odone = pfull + 32, qfull = odone + 32;   // [buffer]
+  const uint32_t sfull = vempty + 8 * S::nv, pfull = sfull + 32, odone = pfull + 32;   // [buffer]
+  const uint32_t qfull = odone + 32;            // [score warp]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::bar + 504);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(odone + 8 * i, 1);
     }
     mbar_init(qfull, 8);
+    mbar_init(qfull + 8, 8);
     fence_mbar_init();
     pdl_trigger();
   }
@@ -293,8 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t qph = 0;
       while (ok && kv8_next(p, w, g)) {
         const Plan pl = make_plan<D>(p, g);
-        wait_all(qfull, qph);
-        qph ^= 1;
+        // Each score warp has a barrier for Q, which goes round only in the segments where the warp
+        // has scores to make (lane 1 has none in a segment of one block): the softmax groups cannot
+        // complete its next phase before they have had those scores, so no phase is passed unseen.
+        if ((i ? pl.steps[1] : pl.steps[0]) > 0) {
+          wait_all(qfull + 8 * i, qph);
+          qph ^= 1;
+        }
         const uint32_t a0 = uniform(q0 + (pl.tiles && i ? kTile : 0));
         // every block in turn, also those of the other lane: a warp that skipped one could take its
         // slot's last phase for the next
@@ -511,7 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         rowf *= exp2i(q_exp(am));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(qfull);
+        if (lane == 0) {
+          mbar_arrive(qfull);
+          if (pl.steps[1] > 0) mbar_arrive(qfull + 8);
+        }
       }
 
       int lo, hi, lo_last, hi_first, t0, t1;

@@ -306,6 +306,24 @@ def test_few_items_over_all_ctas(D, kv, H, nq, B, window):
     p.check_attend(rng.standard_normal((B, nq, H, D)), lens, causal=True, window=window)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_items_of_one_block_between_longer_ones(D):
+    """One CTA after another gets items in which the second lane of the many-rows kernel has no
+    block at all, and then items in which it has some: again and again, with equal bits."""
+    rng = np.random.default_rng(D)
+    B, nq, H = 700, 17, 2
+    p = _filled(rng, 1, D, 300, 2)
+    lens = np.where(np.arange(B) % 6 < 4, rng.integers(0, 65, B), rng.integers(65, 301, B))
+    slots = rng.integers(0, 2, B)
+    Q = rng.standard_normal((B, nq, H, D))
+    p.check_attend(Q, lens, slots=slots)
+    q, n, at = bf16(Q)[0], i32(lens), i32(slots)
+    first = p.c.attend(q, n, slots=at)
+    for _ in range(30):
+        assert torch.equal(p.c.attend(q, n, slots=at), first)
+    p.c.status()
+
+
 def test_scores_of_unlike_size():
     """Block scales far apart, scores far apart, one key that takes all."""
     rng = np.random.default_rng(4)
