@@ -608,8 +608,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_tiles_kernel(const
     }
   }
   if (warp == 0 && p.lse)
-    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] =
-        ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] = kv8_lse(mm, ll);
 }
 
 // Many rows in many parts (few items, so that many CTAs share each): a CTA per (32 rows, item, 32
@@ -675,8 +674,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_parts_kernel(const
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
   if (d == 0 && p.lse)
-    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] =
-        ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] = kv8_lse(mm, ll);
 }
 
 template <int D>

@@ -12,11 +12,11 @@
 //               2^-10 of the largest, else to 2^-17 of it. Two E4M3 products take as long as
 //               one 16-bit product, and K needs no widening.
 //   P           bf16, exp2(s + log2 s_V - m): the V scale enters through the exponent and leaves
-//               the sum in fp32; off by at most 2^-9 of itself; written over S in tensor memory,
+//               the sum in fp32; off by at most 2^-8 of itself; written over S in tensor memory,
 //               from where the second product takes it.
 //   O += P V    kind::f16 on bf16. Four warps widen V blocks to bf16 (exact) in the 128-byte
 //               swizzled K-major layout; both query tiles use each widened block.
-// bf16 has fp32's exponents, so the row's reference m is the maximum of the first block it sees
+// bf16 has fp32's exponents, so the row's reference m comes from the first block it sees
 // and stays unless a block passes it by far (then O in tensor memory is rescaled). At head_dim 64
 // and 128 no other maximum is looked for: the weights' sum shows whether they were too large, and
 // then the block is done once more. With fp16 weights, whose reference may lag by 2^13 at most,
@@ -52,10 +52,14 @@ constexpr int kThreads = 640;
 // Registers: 96 a thread at launch; the softmax groups go up to 168, the three others down to
 // 48 (2 x 128 x 168 + 3 x 128 x 48 = 61440 = 640 x 96).
 
-// The reference moves when a block's largest exponent is above it by more than kLag (head_dim
-// 256), its weights sum to more than kMaxSum (else). A row's sum of exponentials leaves the V
-// scale (>= 2^-60) out of its terms: 2^40 or 64 times 2^32, times 2^60, times 2^24 blocks stay below 2^127.
-constexpr float kLag = 32.0f, kMaxSum = 1099511627776.0f;
+// A row's reference is the largest score of a block, rounded to an integer (so that subtracting it
+// rounds nothing) and lifted by 32 (kKv8Lift). It does not look at V's scales 2^ev, -60 <= ev <= 120:
+// a weight 2^(s + ev - m) is then within fp32's and bf16's range for each of them, down to 2^-34 of
+// the reference's key at ev = -60 (2^-86 at 2^-8, ordinary values) and, with V's 448 * 2^ev below 2^128, with sums
+// over 2^29 keys below 2^127. The reference moves when a block's largest score is above it by more
+// than kLag (head_dim 256), or the weights of a block sum to more than 2^kMaxSum without V's scale
+// (else); by less where V's scale leaves no room for that (kTop: a block's weights stay below 2^kTop).
+constexpr int kLag = 32, kMaxSum = 40 - kKv8Lift, kTop = 95;
 
 template <int D>
 struct Tc {
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c < lo - key0 || c >= hi - key0) x[c] = -INFINITY;
           }
         };
-        // the block's largest score (-infinity times gk stays -infinity: gk > 0)
+        // the reference that the block asks for (-infinity times gk stays -infinity: gk > 0)
         auto largest = [&] {
           float h[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) h[i] = max3(h[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[60 + i]);
-          return fmaf(max3(h[0], h[1], fmaxf(h[2], h[3])), gk, fv);
+          return rintf(max3(h[0], h[1], fmaxf(h[2], h[3])) * gk) + static_cast<float>(kKv8Lift);
         };
         load();
         if (!S::two) {
@@ -603,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (old != m) l *= exp2_approx(m - old);        // (m = -infinity: l is 0)
             m = old;
           }
-          const bool move = mx > m + kLag || (m == -INFINITY && mx > m);
+          const float lag = static_cast<float>(min(kLag, kTop - 6 + kKv8Lift - ev));
+          const bool move = mx > m + lag || (m == -INFINITY && mx > m);
           if (j + 1 < g.n) {
             xch[(j & 1) * 128 + r] = move ? mx : m;
             asm volatile("bar.arrive %0, 64;" ::"r"(1 + grp * 4 + qd) : "memory");
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum = s2.x + s2.y;
           // head_dim <= 128: if the weights are too large for the reference as it stood, once
           // more with the scores read again (a NaN among them comes here too, and stays)
-          move = !(sum <= kMaxSum);
+          move = !(sum <= exp2i(min(kTop, kMaxSum + ev)));
           if (__builtin_expect(!check || !__any_sync(0xffffffffu, move), 1)) break;
           check = false;
           load();
@@ -731,9 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row_ok && (S::two || grp == 0)) {
           if (!g.whole) p.ws_ml[slot * S::rows + tr] = make_float2(m, l);
-          else if (p.lse)
-            p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] =
-                l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          else if (p.lse) p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] = kv8_lse(m, l);
         }
         tc_fence_before();
       }
