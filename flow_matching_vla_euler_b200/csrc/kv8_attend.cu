@@ -24,7 +24,7 @@
 //      for every bf16 value above 2^-24 of the largest.
 //   P: relative to the maximum of its own 64 tokens, fp16(exp2(x - m)): off by at most 2^-11 of p
 //      or 2^-25. The product of the 64 tokens is added to the output in fp32 times
-//      exp2(m - M) s_V.
+//      exp2(m - M) s_V 2^-32 (M the row's reference, 2^-32 for sums of values near bf16's end).
 #include <float.h>
 
 #include "kernels.h"
@@ -35,7 +35,10 @@ namespace vla {
 
 namespace {
 
-constexpr float kMoveBy = 32.0f;             // the reference maximum moves when passed by 2^32
+// The reference is a block's largest score, rounded to an integer. It moves when passed by 2^32, or by
+// less where V's scale 2^ev leaves no room for that (ev <= 120). Outputs are kept times 2^-kKv8Lift:
+// sums of V's 448 * 2^ev over 2^29 keys, with a lag of 2^(kTop - ev), stay below 2^128.
+constexpr int kMoveBy = 32, kTop = 121;
 
 template <int D, int R>
 struct RowsCfg {
@@ -276,6 +279,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
       // ---- weights relative to the block's own maximum
       float fac[kN][2];
       uint2 pb[4][kN];                          // B fragments of the four 16-token groups
+      const float lag = static_cast<float>(min(kMoveBy, kTop - exp_of(sc.y)));
+      const float sv = sc.y * exp2i(-kKv8Lift);
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
         float off[2], gk[2], sum[2] = {0.0f, 0.0f};
@@ -288,9 +293,9 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
           for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
           gk[c] = fmaxf(f[n][c] * sc.x, FLT_MIN);           // (0 would turn a masked score into NaN)
           const float ms = mx * gk[c];
-          const bool move = ms > m[n][c] + kMoveBy || (m[n][c] == -INFINITY && ms > m[n][c]);
+          const bool move = ms > m[n][c] + lag || (m[n][c] == -INFINITY && ms > m[n][c]);
           if (__any_sync(0xffffffffu, move)) {
-            const float nm = move ? ms : m[n][c];
+            const float nm = move ? rintf(ms) : m[n][c];
             const float k = nm == m[n][c] ? 1.0f : exp2_approx(m[n][c] - nm);
             m[n][c] = nm;
             l[n][c] *= k;
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           l[n][c] = fmaf(sum[c], fac[n][c], l[n][c]);
-          fac[n][c] *= sc.y;
+          fac[n][c] *= sv;
         }
       }
       // ---- o += fac * P V
@@ -362,6 +367,9 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], i);
+        // a partial result from here on (kv8.cuh), so o, l and m are lifted alike
+        l[n][c] *= exp2i(-kKv8Lift);
+        m[n][c] += static_cast<float>(kKv8Lift);
         if (gq == 0) ml[warp * R + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
       }
     __syncthreads();
@@ -407,9 +415,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
           const float norm = ll == 0.0f ? 0.0f : 1.0f / ll;
           *reinterpret_cast<__nv_bfloat162*>(p.out + g.b * p.o_st[0] + qi * p.o_st[1] + qh * p.o_st[2] + d) =
               __floats2bfloat162_rn(v.x * norm, v.y * norm);
-          if (d == 0 && p.lse)
-            p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] =
-                ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+          if (d == 0 && p.lse) p.lse[(static_cast<size_t>(g.b) * p.n_q + qi) * p.n_heads + qh] = kv8_lse(mm, ll);
         }
       }
       __syncthreads();
@@ -558,8 +564,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kv8_merge_rows_kernel(const 
       }
     }
   if (lane == 0 && p.lse)
-    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] =
-        ll == 0.0f ? -INFINITY : (m0 + log2f(ll)) * 0.6931471805599453f;
+    p.lse[(static_cast<size_t>(cut.b) * p.n_q + qi) * p.n_heads + qh] = kv8_lse(m0, ll);
 }
 
 // Many rows: a CTA per (32 rows, cut); a lane is a row, a warp takes D / 8 of its columns. Parts

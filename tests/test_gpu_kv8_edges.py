@@ -1,6 +1,9 @@
-"""The 8-bit K/V cache at the ends of its ranges. Bounds as in test_gpu_kv8."""
+"""The 8-bit K/V cache at the ends of its ranges: V scales far apart and at bf16's end. Bounds
+as in test_gpu_kv8."""
 import numpy as np
 import pytest
+
+import flow_matching_vla_euler_b200 as V
 
 from .test_gpu_kv8 import Pair
 
@@ -31,3 +34,23 @@ def test_v_scales_far_apart(D, B, nq, H, spread):
     p.check_attend(Q, lens, slots=slots)
     Q[:, ::3] *= 1e-6                                # equal scores
     p.check_attend(Q, lens, slots=slots, causal=True, window=200)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,nq,H", CALLS)
+def test_v_at_the_end_of_bf16(D, B, nq, H):
+    """Averages of values of 2^127 and more, which no partial sum may pass; with scores that
+    climb from block to block, so that references lag behind."""
+    rng = np.random.default_rng(nq)
+    p = Pair(1, 1, D, 320, 2)
+    Vv = 2.5e38 * rng.choice([1.0, 0.9, 0.5], (1, 2, 320, D))
+    K = rng.standard_normal((1, 2, 320, D))
+    p.write(K, Vv)
+    Q = 0.5 * rng.standard_normal((B, nq, H, D))
+    slots, lens = rng.integers(0, 2, B), rng.integers(280, 321, B)
+    p.check_attend(Q, lens, slots=slots)
+    f = np.repeat([1.0, 6.0, 12.0, 20.0, 30.0], 64)[:, None]
+    p.write(K * f, Vv)
+    p.check_attend(Q, lens, slots=slots)
+    p.write(np.abs(K) * f, Vv)
+    p.check_attend(np.abs(Q), lens, slots=slots, causal=True)
