@@ -194,8 +194,10 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
       for (int i = 0; i < kPl; i += 2) {
         const int d = i * 32 + lane * 2;
         const int m = (d >> 2) & 3, kk = 4 * (d >> 6) + m, tq = (d >> 4) & 3;
+        const float y0 = x[i] * inv, y1 = x[i + 1] * inv;
+        // an infinity becomes NaN: all its scores may be -infinity, which is no key seen
         *reinterpret_cast<uint32_t*>(smem + S::q + ((kk * kN + (r >> 3)) * 32 + (r & 7) * 4 + tq) * 8 + (d & 2) * 2) =
-            pack_h2(x[i] * inv, x[i + 1] * inv);
+            pack_h2(fmaf(y0, 0.0f, y0), fmaf(y1, 0.0f, y1));
       }
       if (lane == 0) rowf[r] = exp2i(e) * p.scale_log2;
     }

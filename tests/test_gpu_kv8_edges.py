@@ -1,5 +1,5 @@
-"""The 8-bit K/V cache at the ends of its ranges: V scales far apart and at bf16's end. Bounds
-as in test_gpu_kv8."""
+"""The 8-bit K/V cache at the ends of its ranges: V scales far apart and at bf16's end, queries
+that are not finite. Bounds as in test_gpu_kv8."""
 import numpy as np
 import pytest
 
@@ -54,3 +54,26 @@ def test_v_at_the_end_of_bf16(D, B, nq, H):
     p.check_attend(Q, lens, slots=slots)
     p.write(np.abs(K) * f, Vv)
     p.check_attend(np.abs(Q), lens, slots=slots, causal=True)
+
+
+# ---- queries that are not finite
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 3, 40])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_infinite_queries_on_keys_of_one_sign(D, nq, bad):
+    """All scores of such a row may be -infinity: NaN all the same, unless it sees no key."""
+    rng = np.random.default_rng(nq)
+    p = Pair(1, 1, D, 200, 1)
+    p.write(0.5 + np.abs(rng.standard_normal((1, 1, 200, D))), rng.standard_normal((1, 1, 200, D)))
+    Q = rng.standard_normal((4, nq, 4, D))
+    Q[0, 0, 1, 3], Q[1, nq - 1, 0], Q[2, 0, 2, D - 1], Q[3, 0, 0, 0] = bad, bad, bad, bad
+    lens = [200, 64, 1, 0]
+    _, got, ls = p.attend(Q, lens, slots=[0] * 4)
+    nan = np.zeros(Q.shape[:3], bool)
+    nan[0, 0, 1] = nan[1, nq - 1, 0] = nan[2, 0, 2] = True
+    assert np.isnan(got[nan]).all() and np.isnan(ls[nan]).all()
+    assert not got[3].any() and np.isneginf(ls[3]).all()
+    Q[~np.isfinite(Q)] = 0.0
+    _, clean, lc = p.attend(Q, lens, slots=[0] * 4)
+    assert np.array_equal(got[~nan], clean[~nan]) and np.array_equal(ls[~nan], lc[~nan])
