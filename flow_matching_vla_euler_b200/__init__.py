@@ -485,7 +485,8 @@ class KVCache8:
     2-byte elements (bf16 values, as torch.bfloat16 or as bits in torch.int16); slots, pos,
     count, kv_len, q_pos and q_count are CUDA int32 tensors [batch], read when the kernels run.
     Calls run on the current stream; one stream at a time uses the cache. Rows that are out of
-    range on the device are left out and raise at the next ``status()``."""
+    range on the device are left out and raise at the next ``status()``; rows of count or q_count
+    0 are padding, whose other entries are not looked at."""
 
     def __init__(self, n_layers: int, n_kv_heads: int, head_dim: int, capacity: int, n_slots: int = 1):
         import torch

@@ -111,6 +111,10 @@ __device__ __forceinline__ Kv8Tile kv8_tile(const Kv8AttendParams& p, int b, int
   r.cnt = p.q_count ? p.q_count[b] : p.n_q;
   r.pos = p.q_pos ? p.q_pos[b] : r.len - r.cnt;
   r.blk0 = r.units = 0;
+  if (r.cnt == 0) {                    // padding: names no slot, length or position
+    r.slot = 0;
+    return r;
+  }
   if (r.slot < 0 || r.slot >= p.c.n_slots || r.len < 0 || r.len > p.c.capacity || r.cnt < 0 || r.cnt > p.n_q ||
       r.pos < -p.n_q || r.pos > p.c.capacity) {
     r.slot = -1;

@@ -448,7 +448,8 @@ VLA_API int vla_pipeline_step(vla_pipeline* p, const uint16_t* K_tok, const uint
  * by one stream at a time, and two captured graphs that use it must not run at once.
  * slots, pos, count, kv_len, q_pos and q_count are DEVICE int32 arrays [batch], read when
  * the kernels run. A row whose entries are out of range is left out (nothing of it is
- * written) and reported by vla_kv8_status.
+ * written) and reported by vla_kv8_status. A row of no tokens (count 0) or no queries (q_count
+ * 0) is padding: its other entries are not looked at.
  */
 typedef struct vla_kv8 vla_kv8;   /* opaque, owned by the library */
 
@@ -486,7 +487,8 @@ typedef struct vla_kv8_rows {
  * that fall among E4M3's subnormals). A token of which a K or V value of one head is not
  * finite is stored for that head as K = NaN, V = 0, and takes no part in the scales: a query
  * that sees it gets NaN, one that does not is not touched by it. Two rows of one call must
- * not name the same slot (the later one is left out and reported). K and V 16-byte aligned.
+ * not name the same slot (the later one is left out and reported; rows of count 0 name none).
+ * K and V 16-byte aligned.
  * Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE (layer, batch or n_tokens out of
  * range), VLA_ERR_STATE (another device is current), VLA_ERR_CUDA.
  */

@@ -1,11 +1,12 @@
 """The 8-bit K/V cache at the ends of its ranges: V scales far apart and at bf16's end, queries
-that are not finite. Bounds as in test_gpu_kv8."""
+that are not finite, padded rows. Bounds as in test_gpu_kv8."""
 import numpy as np
 import pytest
+import torch
 
 import flow_matching_vla_euler_b200 as V
 
-from .test_gpu_kv8 import Pair
+from .test_gpu_kv8 import Pair, _filled, bf16, host, i32, kv_values
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,48 @@ def test_infinite_queries_on_keys_of_one_sign(D, nq, bad):
     Q[~np.isfinite(Q)] = 0.0
     _, clean, lc = p.attend(Q, lens, slots=[0] * 4)
     assert np.array_equal(got[~nan], clean[~nan]) and np.array_equal(ls[~nan], lc[~nan])
+
+
+# ---- rows
+
+@pytest.mark.parametrize("n", [1, 8, 9, 70])
+def test_rows_of_no_tokens_are_padding(n):
+    """Rows of count 0 name no slot and no position that counts, in writes, reads and attention."""
+    rng = np.random.default_rng(n)
+    p = _filled(rng, 2, 64, 200, 3, L=2)
+    K, Vv = (kv_values(rng, (2, 6, n, 128)) for _ in range(2))
+    slots, pos, cnt = [0, 2, 0, 0, -1, 9], [5, 3, 300, 61, 0, -7], [0, n, 0, n, 0, 0]
+    p.c.write(bf16(K)[0], bf16(Vv)[0], slots=i32(slots), pos=i32(pos), count=i32(cnt))
+    p.c.status()
+    p.m.write(bf16(K)[1][:, [1, 3]], bf16(Vv)[1][:, [1, 3]], slots=[2, 0], pos=[3, 61])
+    p.check_read(61 + n, slots=[0])
+    p.check_read(3 + n, slots=[2])
+    out = [torch.full((2, 6, n, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    p.c.read(n, slots=i32(slots), pos=i32(pos), count=i32(cnt), K_out=out[0], V_out=out[1])
+    p.c.status()
+    for w in range(2):
+        ref = p.m.read(w, n, slots=[2, 0], pos=[3, 61], batch=2)
+        assert np.array_equal(host(out[w])[:, [1, 3]], ref)
+        assert torch.all(out[w][:, [0, 2, 4, 5]] == 7.0)
+    # nothing to write anywhere
+    p.c.write(bf16(K)[0], bf16(Vv)[0], slots=i32([-1] * 6), count=i32([0] * 6))
+    p.c.status()
+
+
+@pytest.mark.parametrize("nq", [1, 4, 60])
+def test_rows_of_no_queries_are_padding(nq):
+    rng = np.random.default_rng(nq)
+    p = _filled(rng, 1, 64, 100, 3)
+    Q = rng.standard_normal((5, nq, 2, 64))
+    q, out = bf16(Q)[0], torch.full((5, nq, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((5, nq, 2), 9.0, device="cuda")
+    p.c.attend(q, i32([-3, 100, 1000, 7, 0]), slots=i32([-1, 2, 5, 0, 0]), q_pos=i32([0, 0, 5000, 0, -9999]),
+               q_count=i32([0, nq, 0, nq, 0]), out=out, lse=lse)
+    p.c.status()
+    assert torch.all(out[[0, 2, 4]] == 7.0) and torch.all(lse[[0, 2, 4]] == 9.0)
+    only = p.c.attend(q[[1, 3]], i32([100, 7]), slots=i32([2, 0]), q_pos=i32([0, 0]))
+    assert torch.allclose(out[[1, 3]].float(), only.float(), rtol=2.0 ** -6, atol=1e-6)
+    # (a count that is out of range is still refused)
+    p.c.attend(q, i32([1] * 5), slots=i32([0] * 5), q_count=i32([0, -1, 0, 0, 0]), out=out)
+    with pytest.raises(V.VlaError):
+        p.c.status()
