@@ -581,8 +581,8 @@ class KVCache8:
              K_out=None, V_out=None):
         """Stored tokens as bf16: K, V [n_layers, batch, n_tokens, n_kv_heads * head_dim], int16
         bits as Expert.set_prefix takes them unless K_out and V_out are given. Row b gets count[b]
-        tokens (n_tokens) from position pos[b] (0) of slot slots[b] (b); the output behind them is
-        left as it was (zeros in a tensor made here)."""
+        tokens (n_tokens) from position pos[b] (0) of slot slots[b] (b); the output behind them, and a
+        refused row, is left as it was (zeros in a tensor made here)."""
         n = self.n_layers - int(layer) if n_layers is None else int(n_layers)
         if batch is None:
             given = [t for t in (K_out[0] if K_out is not None and K_out.dim() else None, slots, pos, count)
@@ -596,7 +596,8 @@ class KVCache8:
             if min(shape) < 1:
                 raise ValueError(f"K, V: no such shape {shape}")
             dev = torch.device("cuda", self.device)
-            make = torch.empty if count is None else torch.zeros
+            # zeros where the device may leave rows out
+            make = torch.empty if slots is None and pos is None and count is None else torch.zeros
             K_out = make(shape, dtype=torch.int16, device=dev)
             V_out = make(shape, dtype=torch.int16, device=dev)
         kp, ks = self._strided(K_out, shape, "K_out")
@@ -615,9 +616,10 @@ class KVCache8:
         dense), n_heads a multiple of n_kv_heads; row b sees the first kv_len[b] tokens of slot
         slots[b] (b). Query i stands at position q_pos[b] + i (without q_pos the queries are the
         row's last tokens); ``causal`` hides the keys behind it, ``window`` w > 0 all but its last
-        w. Rows of ``out`` behind q_count[b] are left as they were (zeros in a tensor made here); a
-        query that sees no key gets zeros. ``lse``: optional fp32 [batch, n_q, n_heads] output,
-        log of the sum of exp(score). scale: 1 / sqrt(head_dim) unless given (> 0)."""
+        w. Rows of ``out`` behind q_count[b] and refused rows are left as they were (zeros in a tensor
+        made here, which costs a fill: give ``out`` where time counts); a query that sees no key gets
+        zeros. ``lse``: optional fp32 [batch, n_q, n_heads] output, log of the sum of exp(score).
+        scale: 1 / sqrt(head_dim) unless given (> 0)."""
         import torch
         if q.dim() != 4:
             raise ValueError("q: expected [batch, n_q, n_heads, head_dim]")
@@ -627,7 +629,7 @@ class KVCache8:
         shape = (batch, n_q, n_heads, self.head_dim)
         qp, qs = self._strided(q, shape, "q")
         if out is None:
-            out = (torch.empty if q_count is None else torch.zeros)(shape, dtype=q.dtype, device=q.device)
+            out = torch.zeros(shape, dtype=q.dtype, device=q.device)
         op, os_ = self._strided(out, shape, "out")
         lp = None
         if lse is not None:

@@ -1,5 +1,5 @@
 """The 8-bit K/V cache at the ends of its ranges: V scales far apart and at bf16's end, queries
-that are not finite, padded rows. Bounds as in test_gpu_kv8."""
+that are not finite, padded rows, rows refused on the device. Bounds as in test_gpu_kv8."""
 import numpy as np
 import pytest
 import torch
@@ -123,3 +123,27 @@ def test_rows_of_no_queries_are_padding(nq):
     p.c.attend(q, i32([1] * 5), slots=i32([0] * 5), q_count=i32([0, -1, 0, 0, 0]), out=out)
     with pytest.raises(V.VlaError):
         p.c.status()
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_refused_rows_of_a_fresh_tensor_are_zeros(nq):
+    rng = np.random.default_rng(nq)
+    p = _filled(rng, 1, 64, 100, 3)
+    q, _ = bf16(rng.standard_normal((3, nq, 2, 64)))
+
+    def used_memory(shape):                          # what a new tensor may be given next
+        old = [torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        del old
+
+    for kw in (dict(slots=i32([0, 3, 1])), dict(q_pos=i32([0, 101, 0])), dict(kv_len=i32([100, 101, 5]))):
+        used_memory(q.shape)
+        out = p.c.attend(q, **dict(dict(kv_len=i32([100, 50, 5])), **kw))
+        with pytest.raises(V.VlaError):
+            p.c.status()
+        assert not out[1].any() and out[0].any() and out[2].any()
+    for kw in (dict(slots=i32([0, -1, 1])), dict(pos=i32([0, 91, 0]))):
+        used_memory((1, 3, 10, 64))
+        K, Vv = p.c.read(10, **kw)
+        with pytest.raises(V.VlaError):
+            p.c.status()
+        assert not K[:, 1].any() and not Vv[:, 1].any() and K[:, 0].any() and Vv[:, 2].any()
