@@ -624,8 +624,9 @@ class KVCache8:
         if q.dim() != 4:
             raise ValueError("q: expected [batch, n_q, n_heads, head_dim]")
         batch, n_q, n_heads, _ = q.shape
-        if scale is not None and not float(scale) > 0.0:
-            raise ValueError("scale must be > 0")
+        # (as the library gets it: what fp32 makes 0 would stand for the default)
+        if scale is not None and not ctypes.c_float(float(scale)).value > 0.0:
+            raise ValueError("scale must be > 0 in fp32")
         shape = (batch, n_q, n_heads, self.head_dim)
         qp, qs = self._strided(q, shape, "q")
         if out is None:

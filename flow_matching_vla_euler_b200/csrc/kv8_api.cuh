@@ -17,6 +17,8 @@ struct vla_kv8 {
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Query rows of a tile of the many-rows kernel.
 int kv8_tc_rows(const Kv8Cache& c) { return c.Ds == 256 ? 128 : 256; }
 
@@ -175,7 +177,8 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   if (a->n_q < 1 || a->n_q > (1 << 20)) return fail(VLA_ERR_SHAPE, "n_q %d outside [1, 2^20]", a->n_q);
   if (a->causal != 0 && a->causal != 1) return fail(VLA_ERR_ARG, "causal %d: 0 or 1", a->causal);
   if (a->window < 0 || a->window > (1 << 30)) return fail(VLA_ERR_ARG, "window %d outside [0, 2^30]", a->window);
-  if (!(a->scale >= 0.0f) || std::isinf(a->scale)) return fail(VLA_ERR_ARG, "scale must be finite and >= 0");
+  if (!(a->scale >= 0.0f) || std::isinf(a->scale * kLog2e))
+    return fail(VLA_ERR_ARG, "scale must be >= 0, and finite times log2(e)");
   Kv8AttendParams p{};
   const long long w = static_cast<long long>(a->n_heads) * h->c.D;
   for (int i = 0; i < 2; ++i) {
@@ -205,7 +208,7 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   p.group = a->n_heads / h->c.n_kv;
   p.causal = a->causal;
   p.window = a->window;
-  p.scale_log2 = (a->scale > 0.0f ? a->scale : 1.0f / sqrtf(static_cast<float>(h->c.D))) * 1.4426950408889634f;
+  p.scale_log2 = (a->scale > 0.0f ? a->scale : 1.0f / sqrtf(static_cast<float>(h->c.D))) * kLog2e;
   p.err = h->err;
   p.ws = h->ws;
   p.ws_ml = h->ws_ml;

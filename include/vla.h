@@ -510,7 +510,7 @@ typedef struct vla_kv8_query {
                                        h / (n_heads / n_kv_heads) */
   int causal;                /* 1: query i sees keys j <= q_pos + i; 0: all below kv_len */
   int window;                /* w > 0: only keys j > q_pos + i - w; 0: no window */
-  float scale;               /* of the scores; 0: 1 / sqrt(D) */
+  float scale;               /* of the scores; 0: 1 / sqrt(D); at most FLT_MAX / log2(e) */
   long long q_stride[3], out_stride[3];   /* elements (row, token, head), multiples of 8, all 0:
                                              packed */
 } vla_kv8_query;

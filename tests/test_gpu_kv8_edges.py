@@ -147,3 +147,16 @@ def test_refused_rows_of_a_fresh_tensor_are_zeros(nq):
         with pytest.raises(V.VlaError):
             p.c.status()
         assert not K[:, 1].any() and not Vv[:, 1].any() and K[:, 0].any() and Vv[:, 2].any()
+
+
+# ---- refusals
+
+def test_scales_out_of_range_are_refused():
+    p = _filled(np.random.default_rng(1), 1, 64, 100, 1)
+    q, _ = bf16(np.ones((1, 1, 2, 64)))
+    with pytest.raises(ValueError, match="scale"):
+        p.c.attend(q, i32([100]), scale=1e-50)       # 0 in fp32, which would stand for the default
+    with pytest.raises(V.VlaError) as ei:
+        p.c.attend(q, i32([100]), scale=3e38)        # times log2(e): infinite
+    assert ei.value.code == V.VLA_ERR_ARG
+    p.check_attend(np.ones((1, 1, 2, 64)), [100], scale=1e-40)

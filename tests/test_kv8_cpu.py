@@ -100,6 +100,15 @@ def test_binding_shapes():
         V.KVCache8.attend(c, torch.zeros(2, 1, 4, 32, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("scale", [1e-50, 7e-46, -1.0, 0.0, float("nan")])
+def test_scales_that_fp32_does_not_hold(scale):
+    """A scale that fp32 makes 0 would reach the library as the default."""
+    c = _cache()
+    q = torch.zeros(2, 1, 4, 32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="scale"):
+        V.KVCache8.attend(c, q, torch.zeros(2, dtype=torch.int32), scale=scale)
+
+
 def test_create_without_a_gpu_fails_cleanly(lib):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
