@@ -224,6 +224,9 @@ int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, con
   if (units > 2147483647.0)
     return fail(VLA_ERR_SHAPE, "%.0f units of work (tiles of %d query rows times blocks), at most 2^31 - 1 a call", units,
                 p.tile_rows);
+  // (the kernels number the query rows of a K/V head by an int, to the end of the last tile)
+  if (tiles * p.tile_rows > 2147483647.0)
+    return fail(VLA_ERR_SHAPE, "%.0f query rows a K/V head (n_q * n_heads / n_kv_heads), fewer than 2^31 a call", rows);
   p.tiles = static_cast<int>(tiles);
   p.by_group = FastDiv(p.group);
   p.by_tiles = FastDiv(p.tiles);

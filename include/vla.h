@@ -507,7 +507,8 @@ typedef struct vla_kv8_query {
                                 queries are the row's last tokens, already written) */
   const int *q_count;        /* queries of the row, 0 .. n_q; NULL: n_q */
   int layer, batch, n_q, n_heads;   /* n_heads: a multiple of n_kv_heads; head h reads K/V head
-                                       h / (n_heads / n_kv_heads) */
+                                       h / (n_heads / n_kv_heads); n_q <= 2^20, and
+                                       n_q * n_heads / n_kv_heads < 2^31 */
   int causal;                /* 1: query i sees keys j <= q_pos + i; 0: all below kv_len */
   int window;                /* w > 0: only keys j > q_pos + i - w; 0: no window */
   float scale;               /* of the scores; 0: 1 / sqrt(D); at most FLT_MAX / log2(e) */

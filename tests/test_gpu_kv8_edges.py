@@ -160,3 +160,17 @@ def test_scales_out_of_range_are_refused():
         p.c.attend(q, i32([100]), scale=3e38)        # times log2(e): infinite
     assert ei.value.code == V.VLA_ERR_ARG
     p.check_attend(np.ones((1, 1, 2, 64)), [100], scale=1e-40)
+
+
+def test_more_query_rows_than_an_int_holds_are_refused():
+    """2^20 queries of 2048 heads on one K/V head: refused on the host, nothing is launched."""
+    p = _filled(np.random.default_rng(2), 1, 64, 64, 1)
+    n, out = i32([64]), torch.full((64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    a = V.vla_kv8_query()
+    a.kv_len, a.batch, a.n_q, a.n_heads = n.data_ptr(), 1, 1 << 20, 2048
+    a.q_stride[:], a.out_stride[:] = (0, 0, 8), (8, 8, 8)
+    with pytest.raises(V.VlaError, match="query rows") as ei:
+        V.vla_kv8_attend(p.c.handle, out.data_ptr(), out.data_ptr(), None, a, torch.cuda.current_stream().cuda_stream)
+    assert ei.value.code == V.VLA_ERR_SHAPE
+    p.c.status()
+    assert torch.all(out == 7.0)
