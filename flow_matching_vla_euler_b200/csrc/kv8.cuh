@@ -276,14 +276,15 @@ __host__ __device__ __forceinline__ bool kv8_merge_by_items(const Kv8AttendParam
   return p.batch * p.tiles <= 128 && p.batch * p.tiles * p.c.n_kv < p.grid - 1;
 }
 
-// A row's partial result is (m, l, o): m its reference, a score in bits (base 2), plus kKv8Lift; l the sum of
-// 2^(s - m), o that of 2^(s - m) v. The lift keeps sums of V's largest values within fp32.
+// A row's partial result is (m, l, o): m its reference, a score in bits (base 2); l the sum of
+// 2^(s - m - kKv8Lift), o that of 2^(s - m - kKv8Lift) v. The lift keeps sums of V's largest values
+// within fp32.
 constexpr int kKv8Lift = 32;
-// Natural logarithm of the sum of exp(score) (the lift taken out again first, exactly).
+// Natural logarithm of the sum of exp(score).
 __device__ __forceinline__ float kv8_lse(float m, float l) {
   constexpr float up = 4294967296.0f;
   static_assert(up == static_cast<float>(1ull << kKv8Lift), "2^kKv8Lift");
-  return l == 0.0f ? -INFINITY : ((m - static_cast<float>(kKv8Lift)) + log2f(l * up)) * 0.6931471805599453f;
+  return l == 0.0f ? -INFINITY : (m + log2f(l * up)) * 0.6931471805599453f;
 }
 
 // Few rows (tile_rows 8 or 16) and many (128 or 256).

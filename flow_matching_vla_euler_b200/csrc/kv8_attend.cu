@@ -285,16 +285,21 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
       const float sv = sc.y * exp2i(-kKv8Lift);
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        float off[2], gk[2], sum[2] = {0.0f, 0.0f};
+        float off[2], sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = -INFINITY;
+          // the scores in bits, rounded before the maximum is taken off: fused with that, a product of
+          // 2^28 and more would miss its own rounded value by bits
+          const float gk = fmaxf(f[n][c] * sc.x, FLT_MIN);  // (0 would turn a masked score into NaN)
+          float ms = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) mx = fmaxf(mx, fmaxf(x[h][n][c], x[h][n][c + 2]));
+          for (int h = 0; h < 4; ++h) {
+            x[h][n][c] = __fmul_rn(x[h][n][c], gk);
+            x[h][n][c + 2] = __fmul_rn(x[h][n][c + 2], gk);
+            ms = fmaxf(ms, fmaxf(x[h][n][c], x[h][n][c + 2]));
+          }
 #pragma unroll
-          for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-          gk[c] = fmaxf(f[n][c] * sc.x, FLT_MIN);           // (0 would turn a masked score into NaN)
-          const float ms = mx * gk[c];
+          for (int i = 4; i < 32; i <<= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, i));
           const bool move = ms > m[n][c] + lag || (m[n][c] == -INFINITY && ms > m[n][c]);
           if (__any_sync(0xffffffffu, move)) {
             const float nm = move ? rintf(ms) : m[n][c];
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
           float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            w[c] = exp2_approx(fmaf(x[h][n][c], gk[c & 1], off[c & 1]));
+            w[c] = exp2_approx(x[h][n][c] + off[c & 1]);
             sum[c & 1] += w[c];
           }
           pb[h][n] = make_uint2(transpose8(pack_h2(w[0], w[1])), transpose8(pack_h2(w[2], w[3])));
@@ -369,9 +374,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::warps * 32, 1) kv8_attend_rows_
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], i);
-        // a partial result from here on (kv8.cuh), so o, l and m are lifted alike
-        l[n][c] *= exp2i(-kKv8Lift);
-        m[n][c] += static_cast<float>(kKv8Lift);
+        l[n][c] *= exp2i(-kKv8Lift);       // (as o: a partial result, kv8.cuh)
         if (gq == 0) ml[warp * R + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
       }
     __syncthreads();

@@ -52,14 +52,19 @@ constexpr int kThreads = 640;
 // Registers: 96 a thread at launch; the softmax groups go up to 168, the three others down to
 // 48 (2 x 128 x 168 + 3 x 128 x 48 = 61440 = 640 x 96).
 
-// A row's reference is the largest score of a block, rounded to an integer (so that subtracting it
-// rounds nothing) and lifted by 32 (kKv8Lift). It does not look at V's scales 2^ev, -60 <= ev <= 120:
-// a weight 2^(s + ev - m) is then within fp32's and bf16's range for each of them, down to 2^-34 of
+// A row's reference m is the largest score of a block, rounded to an integer (so that subtracting it
+// rounds nothing). It does not look at V's scales 2^ev, -60 <= ev <= 120: a weight
+// 2^(s + ev - 32 - m) (kKv8Lift = 32) is within fp32's and bf16's range for each of them, down to 2^-34 of
 // the reference's key at ev = -60 (2^-86 at 2^-8, ordinary values) and, with V's 448 * 2^ev below 2^128, with sums
 // over 2^29 keys below 2^127. The reference moves when a block's largest score is above it by more
 // than kLag (head_dim 256), or the weights of a block sum to more than 2^kMaxSum without V's scale
 // (else); by less where V's scale leaves no room for that (kTop: a block's weights stay below 2^kTop).
 constexpr int kLag = 32, kMaxSum = 40 - kKv8Lift, kTop = 95;
+// Factor from which on a block's scores can reach 2^23 bits (its sums of products are below 2^25),
+// where fp32 has no bits left for the fraction and soon none for ev: these are rounded first, the
+// reference is taken off, and then ev is added. (Fused with the subtraction, a product of 2^31 can
+// miss its own rounded value by more than the range of the weights.)
+constexpr float kFarFactor = 0.25f;
 
 template <int D>
 struct Tc {
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float gk = fmaxf(rowf * sc.x, FLT_MIN);       // (never 0: a masked score stays -infinity)
         const int ev = exp_of(sc.y);
-        const float fv = static_cast<float>(ev), un = exp2i(-ev);
+        const float fv = static_cast<float>(ev - kKv8Lift), un = exp2i(-ev);
         sc = scale_of(k + 1);
         float x[64];
         auto load = [&] {
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) h[i] = max3(h[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[60 + i]);
-          return rintf(max3(h[0], h[1], fmaxf(h[2], h[3])) * gk) + static_cast<float>(kKv8Lift);
+          return rintf(max3(h[0], h[1], fmaxf(h[2], h[3])) * gk);
         };
         load();
         if (!S::two) {
@@ -619,16 +624,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum;
         bool move = S::two && m == -INFINITY;
         bool check = S::two;
-        while (true) {
-          if (S::two && __any_sync(0xffffffffu, move)) {
-            const float mx = largest();
-            move_to(move ? fmaxf(m, mx) : m, k, j);
-          }
-          const float off = fv - (m == -INFINITY ? 0.0f : m);
+        // the weights of scores that `score` leaves relative to the reference
+        auto weigh = [&](auto score) {
           float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float2 e = fma2(make_float2(x[c], x[c + 1]), make_float2(gk, gk), make_float2(off, off));
+            const float2 e = score(make_float2(x[c], x[c + 1]));
             const float2 w2 = make_float2(exp2_approx(e.x), exp2_approx(e.y));
             s2 = add2(s2, w2);
             const __nv_bfloat162 h2 = __floats2bfloat162_rn(w2.x, w2.y);
@@ -636,6 +637,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[((c >> 1) & 3) * 8 + (c >> 4) * 2 + ((c >> 3) & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           sum = s2.x + s2.y;
+        };
+        if (__builtin_expect(__any_sync(0xffffffffu, gk >= kFarFactor), 0)) {
+          if (S::two) {
+            const float mx = largest();
+            if (__any_sync(0xffffffffu, mx > m)) move_to(fmaxf(m, mx), k, j);
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+          weigh([&](float2 v) {
+            return make_float2((__fmul_rn(v.x, gk) - ref) + fv, (__fmul_rn(v.y, gk) - ref) + fv);
+          });
+        } else while (true) {
+          if (S::two && __any_sync(0xffffffffu, move)) {
+            const float mx = largest();
+            move_to(move ? fmaxf(m, mx) : m, k, j);
+          }
+          const float off = fv - (m == -INFINITY ? 0.0f : m);
+          weigh([&](float2 v) { return fma2(v, make_float2(gk, gk), make_float2(off, off)); });
           // head_dim <= 128: if the weights are too large for the reference as it stood, once
           // more with the scores read again (a NaN among them comes here too, and stays)
           move = !(sum <= exp2i(min(kTop, kMaxSum + ev)));

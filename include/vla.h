@@ -522,7 +522,7 @@ typedef struct vla_kv8_query {
  * rows behind q_count[b] are left as they were. lse (optional, NULL: none): DEVICE fp32
  * [batch][n_q][n_heads], the logarithm of the sum of exp(score) (-infinity: no key), with
  * which the result can be joined with attention over other keys. Scores, maxima and sums are
- * fp32. Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE, VLA_ERR_STATE (another device
+ * fp32; a row for which scale * max|q| * max|k| passes 2^127 may get NaN. Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE, VLA_ERR_STATE (another device
  * is current), VLA_ERR_CUDA; a bounded wait that gave up is reported by vla_kv8_status.
  */
 VLA_API int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, const vla_kv8_query* args,

@@ -1,5 +1,6 @@
 """The 8-bit K/V cache at the ends of its ranges: V scales far apart and at bf16's end, queries
-that are not finite, padded rows, rows refused on the device. Bounds as in test_gpu_kv8."""
+that are not finite, scores of any size, padded rows, rows refused on the device. Bounds as in
+test_gpu_kv8."""
 import numpy as np
 import pytest
 import torch
@@ -174,3 +175,28 @@ def test_more_query_rows_than_an_int_holds_are_refused():
     assert ei.value.code == V.VLA_ERR_SHAPE
     p.c.status()
     assert torch.all(out == 7.0)
+
+
+# ---- scores
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("B,nq,H", [(1, 1, 4), (1, 10, 2), (1, 40, 2), (160, 40, 2), (20, 80, 2)])
+def test_scores_of_any_size(D, B, nq, H):
+    """Scores from 2^18 to 2^110, of either sign. Each is one product (exact) times the scale, equal
+    keys have equal scores and unlike ones differ by 2^-4 of themselves or more, so the softmax is the
+    mean over the keys that share the largest. Off by the output's and the weights' rounding to
+    bf16, half a step each; lse by two roundings of fp32 and that of the scale, relative."""
+    rng = np.random.default_rng(D + nq)
+    n = 330
+    p = Pair(1, 1, D, n, 2)
+    K = np.zeros((1, 2, n, D))
+    K[..., 3] = rng.choice([1.0, 1.5, 2.0, 3.5, 7.0], (1, 2, n)) * np.array([1.0, -1.0])[None, :, None]
+    p.write(K, rng.standard_normal((1, 2, n, D)))
+    Q = np.zeros((B, nq, H, D))
+    Q[..., 3] = np.exp2(rng.integers(20, 110, (B, nq, H))) * rng.choice([1.0, -1.0], (B, nq, H))
+    slots, lens = rng.integers(0, 2, B), rng.integers(250, n + 1, B)
+    for kw in (dict(), dict(causal=True, window=90)):
+        _, got, ls = p.attend(Q, lens, slots=slots, **kw)
+        ref, rls, mean_v, _, _ = p.m.attend(Q, lens, slots=slots, **kw)
+        assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * mean_v * (1 + 2.0 ** -7))
+        assert np.all(np.abs(ls - rls) <= 2.0 ** -21 * np.abs(rls))
