@@ -52,8 +52,9 @@ constexpr int kThreads = 640;
 // Registers: 96 a thread at launch; the softmax groups go up to 168, the three others down to
 // 48 (2 x 128 x 168 + 3 x 128 x 48 = 61440 = 640 x 96).
 
-// A row's reference m is the largest score of a block, rounded to an integer (so that subtracting it
-// rounds nothing). It does not look at V's scales 2^ev, -60 <= ev <= 120: a weight
+// A row's reference m is the largest score of a block, to a multiple of 2^-12: taking it off ev - 32
+// rounds nothing then, and the largest weight is a power of two to 2^-13 of itself, so that bf16 has
+// it (a row of one key is exact). It does not look at V's scales 2^ev, -60 <= ev <= 120: a weight
 // 2^(s + ev - 32 - m) (kKv8Lift = 32) is within fp32's and bf16's range for each of them, down to 2^-34 of
 // the reference's key at ev = -60 (2^-86 at 2^-8, ordinary values) and, with V's 448 * 2^ev below 2^128, with sums
 // over 2^29 keys below 2^127. The reference moves when a block's largest score is above it by more
@@ -65,6 +66,9 @@ constexpr int kLag = 32, kMaxSum = 40 - kKv8Lift, kTop = 95;
 // reference is taken off, and then ev is added. (Fused with the subtraction, a product of 2^31 can
 // miss its own rounded value by more than the range of the weights.)
 constexpr float kFarFactor = 0.25f;
+__device__ __forceinline__ float on_grid(float s) {      // (from 2^11 on fp32's own steps are wide enough)
+  return fabsf(s) < 2048.0f ? rintf(s * 4096.0f) * (1.0f / 4096.0f) : s;
+}
 
 template <int D>
 struct Tc {
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) h[i] = max3(h[i], x[c + i], x[c + 4 + i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = fmaxf(h[i], x[60 + i]);
-          return rintf(max3(h[0], h[1], fmaxf(h[2], h[3])) * gk);
+          return on_grid(max3(h[0], h[1], fmaxf(h[2], h[3])) * gk);
         };
         load();
         if (!S::two) {

@@ -200,3 +200,22 @@ def test_scores_of_any_size(D, B, nq, H):
         ref, rls, mean_v, _, _ = p.m.attend(Q, lens, slots=slots, **kw)
         assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * mean_v * (1 + 2.0 ** -7))
         assert np.all(np.abs(ls - rls) <= 2.0 ** -21 * np.abs(rls))
+
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("B,nq,H", CALLS)
+def test_a_row_of_one_key_is_that_key(D, B, nq, H):
+    """The only weight is 1 whatever its score, so the output is V as it is stored, bit for bit; and
+    lse is the score, to the error of the scores (2 e_s for the product's and exp2's)."""
+    rng = np.random.default_rng(D + B)
+    p = Pair(1, 1, D, 130, 2)
+    p.write(kv_values(rng, (1, 2, 130, D)), kv_values(rng, (1, 2, 130, D)))
+    slots = rng.integers(0, 2, B)
+    Q = 1.5 * rng.standard_normal((B, nq, H, D))
+    for lens, kw in ((np.ones(B, int), dict()), (rng.integers(nq, 131, B), dict(causal=True, window=1))):
+        qn, got, ls = p.attend(Q, lens, slots=slots, **kw)
+        ref, rls, _, mag, _ = p.m.attend(qn, lens, slots=slots, **kw)
+        assert np.array_equal(got, ref)
+        es = ((D + 8) * 2.0 ** -23 * mag[0] + 2.0 ** -17 * mag[1]) / np.sqrt(D) + 2.0 ** -20
+        ok = np.isfinite(rls)
+        assert np.array_equal(np.isneginf(ls), ~ok) and np.all(np.abs(ls - rls)[ok] <= 2 * es[ok])
