@@ -52,17 +52,17 @@ __device__ __forceinline__ bool make_unit(const Kv8RowsParams& p, unsigned id, U
   u.slot = p.slots ? p.slots[u.b] : u.b;
   const int pos = p.pos ? p.pos[u.b] : 0;
   const int cnt = p.count ? p.count[u.b] : p.n_tokens;
-  if (cnt == 0) return false;              // (padding: names no slot and no position)
   bool bad = u.slot < 0 || u.slot >= p.c.n_slots || pos < 0 || cnt < 0 || cnt > p.n_tokens ||
              pos > p.c.capacity - cnt;
   if (kWrite && p.slots) {   // two rows of one write that name the same slot: the later is refused
     bool dup = false;
-    for (int i = threadIdx.x & 31; i < u.b; i += 32)
-      if (p.slots[i] == u.slot) dup |= !p.count || p.count[i] != 0;
+    // (rows of no tokens name none. Both loads always: behind a branch the second cost 2 % of a write.)
+    const int* n = p.count ? p.count : p.slots;
+    for (int i = threadIdx.x & 31; i < u.b; i += 32) dup |= (p.slots[i] == u.slot) & ((n[i] != 0) | !p.count);
     bad |= __any_sync(0xffffffffu, dup) != 0;
   }
   if (bad) {
-    if ((threadIdx.x & 31) == 0) report(p.err, kKv8BadRow);
+    if ((threadIdx.x & 31) == 0 && cnt != 0) report(p.err, kKv8BadRow);   // (no tokens: padding)
     return false;
   }
   u.blk = pos / kKv8Block + j;
@@ -71,7 +71,7 @@ __device__ __forceinline__ bool make_unit(const Kv8RowsParams& p, unsigned id, U
   u.hi = min(pos + cnt - t0, kKv8Block);
   u.first = t0 + u.lo - pos;
   u.idx = ((static_cast<size_t>(u.l) * p.c.n_slots + u.slot) * p.c.n_kv + u.h) * p.c.nblk + u.blk;
-  return u.lo < u.hi;
+  return cnt > 0 && u.lo < u.hi;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
