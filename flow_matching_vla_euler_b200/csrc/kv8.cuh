@@ -95,7 +95,8 @@ struct Kv8AttendParams {
 // much as some units do (an output in 32 bits to write and to merge, one more tile of Q to bring
 // in): there a cut that lies within `snap` units of an item's end moves to it. 400 rows in tiles of
 // 128 against 64 slots of 788 keys (256 items of up to 13 units, 22 a CTA): 90.1 us with no cut
-// moved, 88.1 with 4 units, 77.8 with 6 and with 12. Items of 64 to 96 units are the same either way.
+// moved, 88.1 with 4 units, 77.8 with 6 and with 12. Items of 64 to 96 units are the same either way;
+// sizes between were not measured.
 
 constexpr int kKv8Snap = 6;        // and no more than a third of a CTA's share
 

@@ -17,8 +17,9 @@
 // operands, but on this architecture it is made of conversions of both operands and fp16
 // products: at head_dim 128 a block took 1390 instructions, with the conversions of K and V
 // written out 1070, transposed about 700. 64 ragged rows of up to 8192 tokens, 8 K/V heads of 128:
-// 163 us the first way, 125 us so; one row of 200001 tokens 102 and 80 us, both 78 % of the copy
-// rate. The rest is the start of the kernel and the merge, some 10 us.)
+// 163 us the first way, 124 us so; one row of 200001 tokens 102 and 80 us, 79 and 78 % of the copy
+// rate. The rest is the start of the kernel and the merge, some 10 us. At head_dim 256 the kernels
+// have all 255 registers and spill 112 bytes a thread with 8 rows, 224 with 16.)
 //   K, V widen to fp16 exactly.
 //   Q: each row times the power of two that brings its largest magnitude to [128, 256): exact
 //      for every bf16 value above 2^-24 of the largest.

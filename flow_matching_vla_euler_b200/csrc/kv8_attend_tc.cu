@@ -9,7 +9,7 @@
 //               64-byte swizzled K-major layout), Q as two E4M3 terms accumulated in one
 //               sum: a row times the power of two that brings its largest magnitude to
 //               [128, 256), hi = e4m3(q), lo = e4m3(q - hi). Exact for bf16 values above
-//               2^-10 of the largest, else to 2^-17 of it. Two E4M3 products take as long as
+//               2^-9 of the largest, else to 2^-17 of it. Two E4M3 products take as long as
 //               one 16-bit product, and K needs no widening.
 //   P           bf16, exp2(s + log2 s_V - m): the V scale enters through the exponent and leaves
 //               the sum in fp32; off by at most 2^-8 of itself; written over S in tensor memory,
@@ -30,12 +30,13 @@
 //     output of its own; the two outputs are joined at the end.
 //   head_dim 256: lane i takes every second block; one output (256 columns), for which the row's
 //     reference maximum goes from block to block between the two groups.
-// 2 x 2048 queries of 32 heads (8 K/V heads, head_dim 128) behind 4096 stored tokens: 0.41 ms, 49 %
+// 2 x 2048 queries of 32 heads (8 K/V heads, head_dim 128) behind 4096 stored tokens: 0.42 ms, 49 %
 // of the measured bf16 rate counted on the formula's products. A step of 64 keys for both tiles
 // takes 1.1 us (2100 clocks) of an SM at head_dim 128 and 1.05 at 64, so it is not the products that
 // bound it: the softmax groups' way through a step does, of which the exponentials fill half (1030
 // clocks for two warps a scheduler) and the loads, stores and waits of a warp the rest. Each new tile
-// costs 8 us more (Q, start of the lanes, output) and a part of one the merge.
+// costs 8 us more (Q, start of the lanes, output) and a part of one the merge. (The softmax groups'
+// code, at 168 registers, spills 200 to 390 bytes a thread.)
 // Warps: 0 and 1 scores, 2 and 3 outputs of lane 0 and 1, 4..7 and 8..11 softmax of lane 0 and 1
 // (one thread a row), 12..15 widening of V, 16 loads of K, 17 loads of V.
 #include <float.h>

@@ -9,9 +9,10 @@
 // E4M3's subnormals round again).
 //
 // Bound by memory: three bytes a value in each direction (two of bf16, one of the cache). Whole
-// blocks are 82 % (64 x 18 x 788 tokens of 256 written and read back, 522 us) and 98 % (32 ragged
+// blocks are 82 % (64 x 18 x 788 tokens of 256 written and read back, 522 us) and 97 % (32 ragged
 // rows of up to 4096 tokens of 8 x 128, 4 layers, read in 376 us) of the copy rate. Writes alone
-// take 268 us of the 522, 79 %: their 32 registers of data a thread leave 32 warps an SM.
+// take 268 us of the 522, 79 %: their 32 registers of data a thread leave 32 warps an SM (and 20 bytes
+// spilled).
 #include <algorithm>
 
 #include "kernels.h"
@@ -319,9 +320,9 @@ __global__ void __launch_bounds__(2 * D, kWriteCtas<D>) kv8_write_kernel(const K
   }
 }
 
-// A write of a few tokens a row (decoding): a CTA per unit, a thread per dim of K and V, so that
-// the units of an ordinary append are on the chip at once: one token of 64 x 18 rows of 256 in
-// 16 us, 29 us with the kernel above, whose blocks wait in four waves. The bytes go straight to their
+// A write of a few tokens a row (decoding): a CTA per unit, a thread per dim of K and V, five CTAs of
+// 256 an SM, so that of an ordinary append's units 740 are on the chip at once: one token of 64 x 18
+// rows of 256 (1152 units) in 16 us, 29 us with the kernel above, whose blocks wait in four waves. The bytes go straight to their
 // places; a block's other bytes are touched only when its scale has to grow. What is left is the
 // latency of lengths, rows and scales one after the other.
 constexpr int kFewTokens = 8;

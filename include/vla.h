@@ -521,8 +521,16 @@ typedef struct vla_kv8_query {
  * bf16 [batch][n_q][n_heads][D], 16-byte aligned. A query that sees no key gets zeros. Output
  * rows behind q_count[b] are left as they were. lse (optional, NULL: none): DEVICE fp32
  * [batch][n_q][n_heads], the logarithm of the sum of exp(score) (-infinity: no key), with
- * which the result can be joined with attention over other keys. Scores, maxima and sums are
- * fp32; a row for which scale * max|q| * max|k| passes 2^127 may get NaN. Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE, VLA_ERR_STATE (another device
+ * which the result can be joined with attention over other keys. A query that is not finite
+ * gets NaN if it sees a key.
+ * Scores, maxima and sums are fp32; a row for which scale * max|q| * max|k| passes 2^127 may
+ * get NaN. The weights that V is multiplied with are rounded: with up to 16 query rows a K/V
+ * head (n_q * n_heads / n_kv_heads; up to 32 in calls of batch * n_kv_heads <= 32) to fp16
+ * relative to the largest of their 64 keys, by at most 2^-11 of themselves (or 2^-25); with
+ * more rows to bf16, by at most 2^-8, and there components of q below 2^-9 of their row's
+ * largest are rounded by up to 2^-17 of it. So a row's last bits depend on the size of the
+ * batch it is in, and on the lengths of the other rows, which decide where its keys are
+ * divided; the same call gives the same bits. Errors (nothing enqueued): VLA_ERR_ARG, VLA_ERR_SHAPE, VLA_ERR_STATE (another device
  * is current), VLA_ERR_CUDA; a bounded wait that gave up is reported by vla_kv8_status.
  */
 VLA_API int vla_kv8_attend(vla_kv8* h, const uint16_t* q, uint16_t* out, float* lse, const vla_kv8_query* args,
